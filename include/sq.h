@@ -338,6 +338,92 @@ sq_status sq_w8a8_accumulate_e4m3(const uint8_t *xq, const uint8_t *wq, int64_t 
                                   sq_stream_t stream);
 
 /*
+ * FP8 (E4M3) with one scale per block of 128: finer than one scale per row,
+ * so one outlier channel costs precision in its own block only.  With
+ * KB = ceil(K / 128) and NB = ceil(N / 128) (the last blocks may be short):
+ *   activations  xq [M][K], x_scale [M][KB]: one scale per token and 128
+ *                channels, x_scale_tb = max_{j in b} |x_tj inv_s_j| / 448;
+ *   weights      wq [N][K], w_scale [NB][KB]: one scale per 128 x 128 block
+ *                of W~ = diag(s) W, its largest magnitude / 448;
+ *   codes        e4m3(v / scale) as above; an all-zero block gives scale 0
+ *                and codes +0.
+ *
+ * sq_quant_act_e4m3_block: as sq_quant_act_e4m3, except that inv_smooth may
+ *   be NULL (no smoothing).
+ * sq_smooth_quant_weight_e4m3_block: E stacked weight matrices (the experts
+ *   that one input feeds; E = 1 for a dense layer), each [N][ldw] (SQ_W_NK),
+ *   expert e starting at row e * N; wq [E][N][K], w_scale [E][NB][KB].  With
+ *   amax [K] they share one smoothing factor, formed as in
+ *   sq_smooth_quant_weight from w_j = the maximum over all E * N rows, and
+ *   smooth, inv_smooth [K] are written.  amax NULL: no smoothing; alpha,
+ *   smooth and inv_smooth are then not used (may be NULL).
+ * sq_w8a8_linear_e4m3_block:
+ *     y_tn = round_yt(sum_b fl(x_scale_tb * w_scale_[n/128]b) * p_tnb),
+ *     p_tnb = sum_{j in block b} xq_tj wq_nj,
+ *   p in fp32 on the tensor cores, the sum over blocks by fp32 fused
+ *   multiply-adds in an order that depends on the shape alone: within
+ *   (KB + 12) * 2^-23 * sum_j |x_j w_j| (x, w the dequantized values) of
+ *   the exact sum, and the same bits on every call.
+ *   M == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N.  No workspace.
+ */
+sq_status sq_quant_act_e4m3_block(const void *x, sq_dtype xt, int64_t M, int64_t K,
+                                  int64_t ldx, const float *inv_smooth, uint8_t *xq,
+                                  float *x_scale, sq_stream_t stream);
+sq_status sq_smooth_quant_weight_e4m3_block(const void *w, sq_dtype wt, int64_t E,
+                                            int64_t N, int64_t K, int64_t ldw,
+                                            const float *amax, float alpha,
+                                            uint8_t *wq, float *w_scale,
+                                            float *smooth, float *inv_smooth,
+                                            sq_stream_t stream);
+sq_status sq_w8a8_linear_e4m3_block(const uint8_t *xq, const float *x_scale,
+                                    const uint8_t *wq, const float *w_scale,
+                                    int64_t M, int64_t N, int64_t K, void *y,
+                                    sq_dtype yt, int64_t ldy, sq_stream_t stream);
+
+/*
+ * Linears over rows grouped by expert (the mixture layers' products): the
+ * rows of xq are sorted by expert, and expert e multiplies rows
+ * offsets[e] .. offsets[e + 1] - 1 by weights of its own.  One launch serves
+ * every expert; the sizes stay on the device.
+ *   xq [T][K]; wq [E][N][K]; y [T][ldy] of type yt OUT.
+ *   offsets [E + 1] int32, DEVICE memory, non-decreasing, within [0, T]
+ *       (any group may be empty; offsets[0] may be above 0).  Rows in no
+ *       group -- before offsets[0] or from offsets[E] on -- are left as they
+ *       were in y.  (Offsets outside [0, T] are clamped and a falling one is
+ *       raised to the largest before it, so that no value of theirs leads to
+ *       an access outside the matrices.)
+ * sq_w8a8_linear_grouped: INT8 codes, x_scale [T], w_scale [E][N]; each
+ *   group's rows as sq_w8a8_linear computes them, bit for bit.  The codes and
+ *   scales of all experts come from one sq_smooth_quant_weight call over the
+ *   stacked [E * N][K] weights (SQ_W_NK), which share one smoothing factor.
+ * sq_w8a8_linear_grouped_e4m3: the same with E4M3 codes (uint8), each group's
+ *   rows within the bound of sq_w8a8_linear_e4m3.
+ * sq_w8a8_linear_grouped_e4m3_block: block scales, x_scale [T][KB], w_scale
+ *   [E][NB][KB], each group's rows within sq_w8a8_linear_e4m3_block's bound.
+ * The E4M3 sums' order depends on T, E, N, K and the offsets alone: the same
+ * bits on every call.
+ * T == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N, E * N < 2^31;
+ * E <= 1024, else SQ_ERR_UNSUPPORTED.  offsets is 4-byte aligned.  No
+ * workspace.
+ */
+sq_status sq_w8a8_linear_grouped(const int8_t *xq, const float *x_scale,
+                                 const int8_t *wq, const float *w_scale,
+                                 const int32_t *offsets, int64_t T, int64_t E,
+                                 int64_t N, int64_t K, void *y, sq_dtype yt,
+                                 int64_t ldy, sq_stream_t stream);
+sq_status sq_w8a8_linear_grouped_e4m3(const uint8_t *xq, const float *x_scale,
+                                      const uint8_t *wq, const float *w_scale,
+                                      const int32_t *offsets, int64_t T, int64_t E,
+                                      int64_t N, int64_t K, void *y, sq_dtype yt,
+                                      int64_t ldy, sq_stream_t stream);
+sq_status sq_w8a8_linear_grouped_e4m3_block(const uint8_t *xq, const float *x_scale,
+                                            const uint8_t *wq, const float *w_scale,
+                                            const int32_t *offsets, int64_t T,
+                                            int64_t E, int64_t N, int64_t K, void *y,
+                                            sq_dtype yt, int64_t ldy,
+                                            sq_stream_t stream);
+
+/*
  * Allocation-free variant of sq_w8a8_linear for decode-shaped calls.
  * (This has no counterpart in the SmoothQuant page; it is a deployment
  * convenience of this library.)

@@ -39,6 +39,8 @@ __all__ = [
     "sq_quant_act_static",
     "sq_smooth_quant_weight_e4m3", "sq_quant_act_e4m3", "sq_w8a8_linear_e4m3", "sq_w8a8_accumulate_e4m3",
     "sq_w8a8_linear_scatter", "sq_quant_act_rotated", "sq_smooth_quant_weight_rotated",
+    "sq_quant_act_e4m3_block", "sq_smooth_quant_weight_e4m3_block", "sq_w8a8_linear_e4m3_block",
+    "sq_w8a8_linear_grouped", "sq_w8a8_linear_grouped_e4m3", "sq_w8a8_linear_grouped_e4m3_block",
 ]
 
 SQ_OK, SQ_ERR_INVALID_ARG, SQ_ERR_UNSUPPORTED, SQ_ERR_CUDA, SQ_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -98,6 +100,12 @@ def lib() -> ctypes.CDLL:
             "sq_w8a8_linear_scatter": [vp, vp, vp, vp, i64, i64, i64, vp, i32, i32, i64, vp, sz, vp],
             "sq_quant_act_rotated": [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp],
             "sq_smooth_quant_weight_rotated": [vp, i32, i64, i64, i64, vp, f32, i64, vp, vp, vp, vp, vp, vp],
+            "sq_quant_act_e4m3_block": [vp, i32, i64, i64, i64, vp, vp, vp, vp],
+            "sq_smooth_quant_weight_e4m3_block": [vp, i32, i64, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp],
+            "sq_w8a8_linear_e4m3_block": [vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, vp],
+            "sq_w8a8_linear_grouped": [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp],
+            "sq_w8a8_linear_grouped_e4m3": [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp],
+            "sq_w8a8_linear_grouped_e4m3_block": [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -414,6 +422,191 @@ def sq_w8a8_accumulate_e4m3(xq: torch.Tensor, wq: torch.Tensor, acc=None, worksp
     _check(lib().sq_w8a8_accumulate_e4m3(_ptr(xq), _ptr(wq), M, N, K, _ptr(acc), acc.stride(0), _ptr(workspace),
                                          wbytes, _stream(stream)), "sq_w8a8_accumulate_e4m3")
     return acc
+
+
+# ---------------------------------------------------------------------------
+# FP8 (E4M3) with one scale per block of 128, and linears over rows grouped
+# by expert.  These calls check every tensor (type, shape, layout, device),
+# run on the tensors' own device whichever is current, and allocate their
+# results on the stream they launch on.
+# ---------------------------------------------------------------------------
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 that cover n values."""
+    return -(-n // 128)
+
+
+def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> None:
+    """t is a contiguous tensor of this type and shape on `device`."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} not supported ({dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_stream(device, stream, call):
+    """call(stream handle) with `device` current and allocations on the stream."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return call(ctypes.c_void_p(stream.cuda_stream))
+
+
+def sq_quant_act_e4m3_block(x: torch.Tensor, inv_smooth=None, xq=None, x_scale=None, stream=None):
+    """(xq [M,K] uint8 E4M3, x_scale [M, ceil(K/128)] = absmax/448 per token and
+    128 channels) of x * inv_smooth (None: of x)."""
+    _rowmajor(x, "x")
+    M, K = x.shape
+    dt, dev = _dtype(x, "x"), x.device
+    if inv_smooth is not None:
+        _expect(inv_smooth, "inv_smooth", torch.float32, (K,), dev)
+    if xq is not None:
+        _expect(xq, "xq", torch.uint8, (M, K), dev)
+    if x_scale is not None:
+        _expect(x_scale, "x_scale", torch.float32, (M, _blocks(K)), dev)
+
+    def call(st):
+        q = torch.empty((M, K), dtype=torch.uint8, device=dev) if xq is None else xq
+        s = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev) if x_scale is None else x_scale
+        _check(lib().sq_quant_act_e4m3_block(x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K,
+                                             None if inv_smooth is None else inv_smooth.data_ptr(), q.data_ptr(),
+                                             s.data_ptr(), st), "sq_quant_act_e4m3_block")
+        return q, s
+    return _on_stream(dev, stream, call)
+
+
+def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float = 0.5, wq=None, w_scale=None,
+                                      smooth=None, inv_smooth=None, stream=None):
+    """(wq, w_scale, s [K], inv_s [K]) with one E4M3 scale per 128 x 128 block of
+    diag(s) W.  w is [N, K] (nn.Linear layout) or, for the experts one input
+    feeds, [E, N, K] (they share s); wq has w's shape (uint8), w_scale is
+    [(E,) ceil(N/128), ceil(K/128)].  amax None: no smoothing, s and inv_s are
+    returned as given (None)."""
+    if w.dim() not in (2, 3) or w.stride(-1) != 1:
+        raise ValueError("w must be a 2-D or 3-D tensor with unit column stride")
+    if not w.is_cuda:
+        raise ValueError("w must be on a CUDA device")
+    E, (N, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
+    ldw = w.stride(-2) if N > 1 else (w.stride(0) if w.dim() == 3 and E > 1 else K)
+    if w.dim() == 3 and E > 1 and w.stride(0) != N * ldw:
+        raise ValueError("w's experts must follow one another (stride(0) == N * stride(1))")
+    dt, dev = _dtype(w, "w"), w.device
+    scale_shape = (*w.shape[:-2], _blocks(N), _blocks(K))
+    if wq is not None:
+        _expect(wq, "wq", torch.uint8, w.shape, dev)
+    if w_scale is not None:
+        _expect(w_scale, "w_scale", torch.float32, scale_shape, dev)
+    for t, name in ((amax, "amax"), (smooth, "smooth"), (inv_smooth, "inv_smooth")):
+        if t is not None:
+            _expect(t, name, torch.float32, (K,), dev)
+
+    def call(st):
+        q = torch.empty(w.shape, dtype=torch.uint8, device=dev) if wq is None else wq
+        sc = torch.empty(scale_shape, dtype=torch.float32, device=dev) if w_scale is None else w_scale
+        s, inv = smooth, inv_smooth
+        if amax is not None:
+            s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else s
+            inv = torch.empty(K, dtype=torch.float32, device=dev) if inv is None else inv
+        _check(lib().sq_smooth_quant_weight_e4m3_block(_ptr(w), dt, E, N, K, ldw, _ptr(amax), ctypes.c_float(alpha),
+                                                       _ptr(q), _ptr(sc), _ptr(s), _ptr(inv), st),
+               "sq_smooth_quant_weight_e4m3_block")
+        return q, sc, s, inv
+    return _on_stream(dev, stream, call)
+
+
+def _out_matrix(y, T: int, N: int, out_dtype, dev):
+    """y checked, or None for one that the caller allocates; the output type."""
+    if y is None:
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype {out_dtype} not supported (float32/float16/bfloat16)")
+        return out_dtype
+    _rowmajor(y, "y")
+    _dtype(y, "y")
+    if y.shape != (T, N):
+        raise ValueError(f"y must have shape {(T, N)}, not {tuple(y.shape)}")
+    if y.device != dev:
+        raise ValueError(f"y must be on {dev}, not {y.device}")
+    return y.dtype
+
+
+def sq_w8a8_linear_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                              out_dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """y [M,N] = dequantized xq times dequantized wq^T for block-scaled E4M3
+    codes: x_scale [M, ceil(K/128)], w_scale [ceil(N/128), ceil(K/128)]."""
+    _rowmajor(xq, "xq")
+    M, K = xq.shape
+    N, dev = wq.shape[0], xq.device
+    _expect(xq, "xq", torch.uint8, (M, K), dev)
+    _expect(wq, "wq", torch.uint8, (N, K), dev)
+    _expect(x_scale, "x_scale", torch.float32, (M, _blocks(K)), dev)
+    _expect(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
+    dt = _out_matrix(y, M, N, out_dtype, dev)
+
+    def call(st):
+        out = torch.empty((M, N), dtype=dt, device=dev) if y is None else y
+        _check(lib().sq_w8a8_linear_e4m3_block(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                                               M, N, K, out.data_ptr(), _DT[dt], out.stride(0) if M > 1 else N, st),
+               "sq_w8a8_linear_e4m3_block")
+        return out
+    return _on_stream(dev, stream, call)
+
+
+def _grouped(name: str, code_dtype, block: bool, xq, x_scale, wq, w_scale, offsets, out_dtype, y, stream):
+    _rowmajor(xq, "xq")
+    if wq.dim() != 3:
+        raise ValueError("wq must be a 3-D tensor [E, N, K]")
+    T, K = xq.shape
+    E, N, dev = wq.shape[0], wq.shape[1], xq.device
+    _expect(xq, "xq", code_dtype, (T, K), dev)
+    _expect(wq, "wq", code_dtype, (E, N, K), dev)
+    _expect(x_scale, "x_scale", torch.float32, (T, _blocks(K)) if block else (T,), dev)
+    _expect(w_scale, "w_scale", torch.float32, (E, _blocks(N), _blocks(K)) if block else (E, N), dev)
+    _expect(offsets, "offsets", torch.int32, (E + 1,), dev)
+    dt = _out_matrix(y, T, N, out_dtype, dev)
+
+    def call(st):
+        out = torch.empty((T, N), dtype=dt, device=dev) if y is None else y
+        _check(getattr(lib(), name)(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                                    offsets.data_ptr(), T, E, N, K, out.data_ptr(), _DT[dt],
+                                    out.stride(0) if T > 1 else N, st), name)
+        return out
+    return _on_stream(dev, stream, call)
+
+
+def sq_w8a8_linear_grouped(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                           offsets: torch.Tensor, out_dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
+    """y [T,N]: rows offsets[e] .. offsets[e+1] of the int8 codes xq [T,K] times
+    expert e's wq[e]^T (wq [E,N,K]), scaled by x_scale [T] and w_scale [E,N].
+    offsets [E+1] is int32 on the device, non-decreasing, and is not read on
+    the host.  Rows in no group keep what y held (an allocated y:
+    unspecified values)."""
+    return _grouped("sq_w8a8_linear_grouped", torch.int8, False, xq, x_scale, wq, w_scale, offsets, out_dtype, y,
+                    stream)
+
+
+def sq_w8a8_linear_grouped_e4m3(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                                offsets: torch.Tensor, out_dtype=torch.bfloat16, y=None,
+                                stream=None) -> torch.Tensor:
+    """sq_w8a8_linear_grouped for E4M3 codes (uint8)."""
+    return _grouped("sq_w8a8_linear_grouped_e4m3", torch.uint8, False, xq, x_scale, wq, w_scale, offsets, out_dtype,
+                    y, stream)
+
+
+def sq_w8a8_linear_grouped_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
+                                      w_scale: torch.Tensor, offsets: torch.Tensor, out_dtype=torch.bfloat16,
+                                      y=None, stream=None) -> torch.Tensor:
+    """sq_w8a8_linear_grouped for block-scaled E4M3 codes (uint8): x_scale
+    [T, ceil(K/128)], w_scale [E, ceil(N/128), ceil(K/128)]."""
+    return _grouped("sq_w8a8_linear_grouped_e4m3_block", torch.uint8, True, xq, x_scale, wq, w_scale, offsets,
+                    out_dtype, y, stream)
 
 
 # Size of the scratch array compiled into libsq.so for the allocation-free

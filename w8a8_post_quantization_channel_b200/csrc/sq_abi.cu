@@ -364,6 +364,102 @@ sq_status sq_w8a8_accumulate_e4m3(const uint8_t *xq, const uint8_t *wq, int64_t 
                          ldacc, workspace, workspace_bytes, sq::QFmt::E4M3, stream);
 }
 
+sq_status sq_quant_act_e4m3_block(const void *x, sq_dtype xt, int64_t M, int64_t K, int64_t ldx,
+                                  const float *inv_smooth, uint8_t *xq, float *x_scale, sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  if (!valid_dtype(xt) || K <= 0 || K % 16 != 0 || K >= kMaxDim || M < 0 || M >= kMaxDim) return SQ_ERR_INVALID_ARG;
+  if (ldx < K || (ldx * dsize(xt)) % 16 != 0) return SQ_ERR_INVALID_ARG;
+  if (inv_smooth != nullptr && !valid_vec(inv_smooth)) return SQ_ERR_INVALID_ARG;
+  if (M == 0) return SQ_OK;
+  if (!valid_matrix(x, xt, M, K, ldx) || !valid_vec(xq) || !valid_vec(x_scale)) return SQ_ERR_INVALID_ARG;
+  return from_cuda(sq::launch_quant_act_block(x, xt, M, K, ldx, inv_smooth, xq, x_scale, (cudaStream_t)stream));
+}
+
+sq_status sq_smooth_quant_weight_e4m3_block(const void *w, sq_dtype wt, int64_t E, int64_t N, int64_t K, int64_t ldw,
+                                            const float *amax, float alpha, uint8_t *wq, float *w_scale, float *smooth,
+                                            float *inv_smooth, sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  if (!valid_dtype(wt) || E <= 0 || N <= 0 || K <= 0 || K % 16 != 0 || N % 16 != 0) return SQ_ERR_INVALID_ARG;
+  if (E >= kMaxDim || N >= kMaxDim || K >= kMaxDim || E * N >= kMaxDim) return SQ_ERR_INVALID_ARG;
+  if (!valid_matrix(w, wt, E * N, K, ldw) || !valid_vec(wq) || !valid_vec(w_scale)) return SQ_ERR_INVALID_ARG;
+  if (amax != nullptr) {
+    if (!(alpha >= 0.0f && alpha <= 1.0f)) return SQ_ERR_INVALID_ARG;
+    if (!valid_vec(amax) || !valid_vec(smooth) || !valid_vec(inv_smooth)) return SQ_ERR_INVALID_ARG;
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  if (amax != nullptr) {
+    // w_j = max over every expert's rows into `smooth`, then s_j and 1/s_j
+    cudaError_t e = sq::launch_zero_fill(smooth, K, st);
+    if (e == cudaSuccess) e = sq::launch_absmax_cols(w, wt, E * N, K, ldw, nullptr, smooth, true, st);
+    if (e == cudaSuccess) e = sq::launch_smooth_factor(amax, smooth, inv_smooth, K, alpha, st);
+    if (e != cudaSuccess) return SQ_ERR_CUDA;
+  }
+  return from_cuda(
+      sq::launch_quant_weight_block(w, wt, E, N, K, ldw, amax != nullptr ? smooth : nullptr, wq, w_scale, st));
+}
+
+// Checks shared by the grouped linears and the dense block-scaled one, then
+// the launch.  `grouped`: offsets are required.
+static sq_status grouped_impl(const void *xq, const float *x_scale, const void *wq, const float *w_scale,
+                              const int32_t *offsets, bool grouped, int64_t T, int64_t E, int64_t N, int64_t K, void *y,
+                              sq_dtype yt, int64_t ldy, sq::GScale scale, sq_stream_t stream) {
+  if (!valid_dtype(yt)) return SQ_ERR_INVALID_ARG;
+  if (T < 0 || T >= kMaxDim || E <= 0 || E >= kMaxDim || N <= 0 || N >= kMaxDim || K <= 0 || K >= kMaxDim)
+    return SQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % 16 != 0 || E * N >= kMaxDim) return SQ_ERR_INVALID_ARG;
+  if (ldy < N || (ldy * dsize(yt)) % 16 != 0) return SQ_ERR_INVALID_ARG;
+  if (!valid_vec(wq) || !valid_vec(w_scale)) return SQ_ERR_INVALID_ARG;
+  if (grouped && (offsets == nullptr || (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0)) return SQ_ERR_INVALID_ARG;
+  if (E > sq::kMaxExperts) return SQ_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits; the smallest are 16 rows by 128 columns
+  if ((T / 16 + E) * ((N + 127) / 128) >= kMaxDim) return SQ_ERR_UNSUPPORTED;
+  if (T == 0) return SQ_OK;
+  if (!valid_vec(xq) || !valid_vec(x_scale) || !valid_vec(y)) return SQ_ERR_INVALID_ARG;
+  sq::GroupedArgs a{};
+  a.xq = xq;
+  a.x_scale = x_scale;
+  a.wq = wq;
+  a.w_scale = w_scale;
+  a.offsets = offsets;
+  a.T = T;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  a.y = y;
+  a.kind = yt == SQ_F32 ? sq::OutKind::F32 : yt == SQ_F16 ? sq::OutKind::F16 : sq::OutKind::BF16;
+  a.ldy = ldy;
+  return from_cuda(sq::launch_grouped(a, scale, (cudaStream_t)stream));
+}
+
+sq_status sq_w8a8_linear_e4m3_block(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
+                                    int64_t M, int64_t N, int64_t K, void *y, sq_dtype yt, int64_t ldy,
+                                    sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  return grouped_impl(xq, x_scale, wq, w_scale, nullptr, false, M, 1, N, K, y, yt, ldy, sq::GScale::Block, stream);
+}
+
+sq_status sq_w8a8_linear_grouped(const int8_t *xq, const float *x_scale, const int8_t *wq, const float *w_scale,
+                                 const int32_t *offsets, int64_t T, int64_t E, int64_t N, int64_t K, void *y,
+                                 sq_dtype yt, int64_t ldy, sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  return grouped_impl(xq, x_scale, wq, w_scale, offsets, true, T, E, N, K, y, yt, ldy, sq::GScale::I8, stream);
+}
+
+sq_status sq_w8a8_linear_grouped_e4m3(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
+                                      const int32_t *offsets, int64_t T, int64_t E, int64_t N, int64_t K, void *y,
+                                      sq_dtype yt, int64_t ldy, sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  return grouped_impl(xq, x_scale, wq, w_scale, offsets, true, T, E, N, K, y, yt, ldy, sq::GScale::E4M3, stream);
+}
+
+sq_status sq_w8a8_linear_grouped_e4m3_block(const uint8_t *xq, const float *x_scale, const uint8_t *wq,
+                                            const float *w_scale, const int32_t *offsets, int64_t T, int64_t E,
+                                            int64_t N, int64_t K, void *y, sq_dtype yt, int64_t ldy,
+                                            sq_stream_t stream) {
+  SQ_TRACE_CALL();
+  return grouped_impl(xq, x_scale, wq, w_scale, offsets, true, T, E, N, K, y, yt, ldy, sq::GScale::Block, stream);
+}
+
 sq_status sq_selftest_wait_timeout(int limit_ms, sq_stream_t stream) {
   SQ_TRACE_CALL();
   if (limit_ms < 1 || limit_ms > 5000) return SQ_ERR_INVALID_ARG;

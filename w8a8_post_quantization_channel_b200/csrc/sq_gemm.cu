@@ -1385,6 +1385,10 @@ cudaError_t gemm_dispatch(const int8_t *xq, const float *x_scale, const int8_t *
 
 }  // namespace
 
+bool make_code_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows) {
+  return make_tmap_i8(m, static_cast<const int8_t *>(base), rows, cols, box_rows);
+}
+
 bool w8a8_decode_uses_workspace(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || M > kDecodeMaxM) return false;
   int dev = 0;

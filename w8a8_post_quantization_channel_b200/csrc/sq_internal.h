@@ -1,6 +1,7 @@
 // sq_internal.h -- launchers shared between the ABI shim and the kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 #include <stddef.h>
@@ -80,6 +81,15 @@ cudaError_t launch_rot_quant_rows(const void *x, sq_dtype xt, int64_t rows, int6
                                   const float *col_scale, int logn, const float *cs, int8_t *q, float *row_scale_out,
                                   cudaStream_t st);
 
+// E4M3 with one scale per token and 128 channels: scale [rows][ceil(cols/128)].
+// inv_s may be null (no smoothing).
+cudaError_t launch_quant_act_block(const void *x, sq_dtype xt, int64_t rows, int64_t cols, int64_t ld,
+                                   const float *inv_s, uint8_t *q, float *scale, cudaStream_t st);
+// E4M3 with one scale per 128 x 128 block of diag(s) W, W [E][N][ld]: scale
+// [E][ceil(N/128)][ceil(K/128)].  s may be null.
+cudaError_t launch_quant_weight_block(const void *w, sq_dtype wt, int64_t E, int64_t N, int64_t K, int64_t ld,
+                                      const float *s, uint8_t *q, float *scale, cudaStream_t st);
+
 // Output kinds of the tensor-core GEMM epilogue (I32: the raw 32-bit
 // accumulator -- an int32 sum for INT8 operands, an f32 sum for E4M3).
 enum class OutKind { F32, F16, BF16, I32 };
@@ -107,5 +117,26 @@ size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 // Whether the decode-shaped product (1 <= M <= 64) of this shape takes the
 // stream-K kernel on the current device.
 bool w8a8_decode_uses_workspace(int64_t M, int64_t N, int64_t K);
+
+// 2-D tensor map over a [rows][cols] row-major matrix of 8-bit codes, box of
+// box_rows x 128 bytes with 128-byte swizzling; false if it cannot be made.
+bool make_code_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int box_rows);
+
+// Linears over rows grouped by expert (offsets [E + 1] on the device; null:
+// one group of all T rows), and how their codes are scaled.
+enum class GScale { I8, E4M3, Block };
+constexpr int kMaxExperts = 1024;
+struct GroupedArgs {
+  const void *xq;
+  const float *x_scale;
+  const void *wq;
+  const float *w_scale;
+  const int32_t *offsets;
+  int64_t T, E, N, K;
+  void *y;
+  OutKind kind;
+  int64_t ldy;
+};
+cudaError_t launch_grouped(const GroupedArgs &a, GScale scale, cudaStream_t st);
 
 }  // namespace sq
