@@ -438,26 +438,29 @@ def _blocks(n: int) -> int:
 
 def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> None:
     """t is a contiguous tensor of this type and shape on `device`."""
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} not supported ({dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _on_stream(device, stream, call):
     """call(stream handle) with `device` current and allocations on the stream."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        # the handle alone: building torch's stream object costs more than a launch
+        index = device.index
+        if index == torch._C._cuda_getDevice():
+            return call(torch._C._cuda_getCurrentRawStream(index))
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
-        return call(ctypes.c_void_p(stream.cuda_stream))
+        return call(stream.cuda_stream)
 
 
 def sq_quant_act_e4m3_block(x: torch.Tensor, inv_smooth=None, xq=None, x_scale=None, stream=None):
