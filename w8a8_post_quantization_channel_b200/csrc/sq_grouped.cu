@@ -104,11 +104,23 @@ __device__ __forceinline__ void build_groups(const Groups &g, const int32_t *__r
   __syncthreads();
 }
 
-// Where a tile lies.  find() is called with tile numbers that never fall.
+// Where a tile lies; find() starts from the group of the tile before.
 struct Place {
   int e = 0, row0 = 0, rows = 0, mb = 0, nb = 0;
-  __device__ __forceinline__ void find(const Groups &g, int tile, int tile_rows) {
-    while (tile >= g.tile[e + 1]) ++e;
+  __device__ __forceinline__ void find(const Groups &g, int E, int tile, int tile_rows) {
+    if (tile < g.tile[e]) e = 0;
+    if (tile >= g.tile[e + 1]) {  // the first group that ends beyond the tile
+      int lo = e + 1, hi = E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tile < g.tile[mid + 1]) {
+          hi = mid;
+        } else {
+          lo = mid + 1;
+        }
+      }
+      e = lo;
+    }
     row0 = g.row[e];
     rows = g.row[e + 1] - row0;
     const int nm = ceil_div_dev(rows, tile_rows), local = tile - g.tile[e];
@@ -179,11 +191,11 @@ struct RowStore {
   }
 };
 
-template <int CG, int BN>
-struct GSmem {
+constexpr int kPairRows = 256, kPairCols = 256;
+struct PairTileSmem {
   static constexpr int kStages = 5;
   static constexpr uint32_t kA = 128 * kBlk;        // this CTA's rows of Xq
-  static constexpr uint32_t kB = (BN / CG) * kBlk;  // this CTA's share of the tile's rows of Wq
+  static constexpr uint32_t kB = (kPairCols / 2) * kBlk;  // this CTA's half of the tile's rows of Wq
   static constexpr uint32_t kRing = kStages * (kA + kB);
   static constexpr uint32_t kStaging = kEpiWarps * kStageBytes;
   static constexpr uint32_t kTable = 2 * (kMaxExperts + 1) * 4 + 8;
@@ -197,20 +209,18 @@ struct GSmem {
 __device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
 
-// Persistent over (128 CG) x BN tiles of Y, one CTA per SM.  CG = 2: a pair of
-// CTAs works on one tile (tcgen05 cta_group::2), each with 128 rows of Xq and
-// half of the tile's rows of Wq in its shared memory; the leader's MMA thread
-// drives both.  Warp 0 loads, warp 1 issues the MMAs, warps 4-11 (two per
+// Persistent over 256 x 256 tiles of Y: a pair of CTAs works on one tile
+// (tcgen05 cta_group::2), each with 128 rows of Xq and half of the tile's rows
+// of Wq in its shared memory; the leader's MMA thread drives both.  Warp 0 loads, warp 1 issues the MMAs, warps 4-11 (two per
 // TMEM lane quarter, each half of the columns) dequantize and store.
-template <int CG, int BN, GScale SC, OutKind KIND>
+template <GScale SC, OutKind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const float *__restrict__ x_scale, const float *__restrict__ w_scale,
                         const int32_t *__restrict__ offsets, uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N,
                         int K, unsigned *err) {
-  using L = GSmem<CG, BN>;
+  using L = PairTileSmem;
   constexpr bool kF8 = SC != GScale::I8, kBlock = SC == GScale::Block;
-  constexpr int kRows = 128 * CG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sA = smem;
@@ -228,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   g.tile = g.row + kMaxExperts + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
+  const int rank = (int)cluster_ctarank();
   const bool leader = rank == 0;
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
-  const int ntn = (N + BN - 1) / BN;
+  const int unit = blockIdx.x / 2, units = gridDim.x / 2;
+  const int ntn = (N + kPairCols - 1) / kPairCols;
   const int nk = (K + kBlk - 1) / kBlk;
 
   if (threadIdx.x == 0) {
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kEpiWarps * CG);  // the epilogue warps of every CTA on the tile
+      mbar_init(&tempty[b], kEpiWarps * 2);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -250,25 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmB);
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      tmem_alloc_pair(tmem_slot, 2 * BN);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, 2 * BN);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, 2 * kPairCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  if constexpr (CG == 2) {
-    cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
-  } else {
-    __syncthreads();
-  }
+  cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // prologue done; the previous kernel's results are visible from here on
   pdl_trigger();
-  build_groups(g, offsets, E, T, kRows, ntn);
+  build_groups(g, offsets, E, T, kPairRows, ntn);
   const int tiles = g.tile[E];
 
   if (warp < 4) regs_give();
@@ -279,26 +280,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Place p;
       for (int tile = unit; tile < tiles && ok; tile += units) {
-        p.find(g, tile, kRows);
-        const int row_a = p.row0 + p.mb * kRows + rank * 128, row_b = p.e * N + p.nb * BN + rank * (BN / CG);
+        p.find(g, E, tile, kPairRows);
+        const int row_a = p.row0 + p.mb * kPairRows + rank * 128, row_b = p.e * N + p.nb * kPairCols + rank * (kPairCols / 2);
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, err)) {
             ok = false;
             break;
           }
-          if (leader) {  // its barrier counts every CTA's copies
-            mbar_arrive_expect_tx(&full[stage], CG * (L::kA + L::kB));
+          if (leader) {  // its barrier counts both CTAs' copies
+            mbar_arrive_expect_tx(&full[stage], 2 * (L::kA + L::kB));
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
-          if constexpr (CG == 2) {
-            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-            tma_load_2d_pair(&tmA, bar, sA + stage * L::kA, kb * kBlk, row_a);
-            tma_load_2d_pair(&tmB, bar, sB + stage * L::kB, kb * kBlk, row_b);
-          } else {
-            tma_load_2d(&tmA, &full[stage], sA + stage * L::kA, kb * kBlk, row_a);
-            tma_load_2d(&tmB, &full[stage], sB + stage * L::kB, kb * kBlk, row_b);
-          }
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          tma_load_2d_pair(&tmA, bar, sA + stage * L::kA, kb * kBlk, row_a);
+          tma_load_2d_pair(&tmB, bar, sB + stage * L::kB, kb * kBlk, row_b);
           if (++stage == L::kStages) {
             stage = 0;
             phase ^= 1;
@@ -310,17 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, nullptr, err);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------- MMA issuer ----------------
-      auto commit = [](uint64_t *bar) {
-        if constexpr (CG == 2) {
-          umma_commit_both(bar);
-        } else {
-          umma_commit(bar);
-        }
-      };
-      constexpr uint32_t idesc = idesc8<kF8>(kRows, BN);
+      constexpr uint32_t idesc = idesc8<kF8>(kPairRows, kPairCols);
       uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
       bool ok = true;
       for (int tile = unit; tile < tiles && ok; tile += units) {
@@ -338,17 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + stage * L::kA));
           const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + stage * L::kB));
 #pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k) {
-            const uint32_t add = (k != 0 || !first) ? 1u : 0u;
-            if constexpr (CG == 2) {
-              umma8_pair<kF8>(tmem_base + ab * BN, a0 + 2 * k, b0 + 2 * k, idesc, add);
-            } else {
-              umma8<kF8>(tmem_base + ab * BN, a0 + 2 * k, b0 + 2 * k, idesc, add);
-            }
-          }
-          commit(&empty[stage]);
+          for (int k = 0; k < kBlk / 32; ++k)
+            umma8_pair<kF8>(tmem_base + ab * kPairCols, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
+          umma_commit_both(&empty[stage]);
           if (last) {
-            if (!kBlock) commit(&tfull[ab]);
+            if (!kBlock) umma_commit_both(&tfull[ab]);
             ab ^= 1;
             if (ab == 0) aphase ^= 1;
           }
@@ -359,31 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // every MMA issued above must finish before TMEM is released
-      if constexpr (CG == 2) {
-        umma_commit_pair(mapa_shared(smem_u32(drain), 0));
-      } else {
-        umma_commit(drain);
-      }
+      umma_commit_pair(mapa_shared(smem_u32(drain), 0));
       mbar_wait(drain, 0, nullptr, err);
     }
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     regs_take();
-    constexpr int kCols = BN / 2;  // columns of this warp
+    constexpr int kCols = kPairCols / 2;  // columns of this warp
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kCols;
-    const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(tempty), 0) : 0u;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
     auto release = [&](uint32_t b) {  // accumulator b may be overwritten, as far as this warp goes
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) {
-          mbar_arrive_remote(tempty0 + b * 8);
-        } else {
-          mbar_arrive(&tempty[b]);
-        }
-      }
+      if (lane == 0) mbar_arrive_remote(tempty0 + b * 8);
     };
     RowStore<KIND> out;
     out.stage = staging + (warp - 4) * kStageBytes;
@@ -396,10 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Place p;
     for (int tile = unit; tile < tiles && ok; tile += units) {
-      p.find(g, tile, kRows);
-      out.row0 = p.row0 + p.mb * kRows + rank * 128 + quarter * 32;
+      p.find(g, E, tile, kPairRows);
+      out.row0 = p.row0 + p.mb * kPairRows + rank * 128 + quarter * 32;
       out.row_end = p.row0 + p.rows;
-      const int n0 = p.nb * BN + half * kCols;
+      const int n0 = p.nb * kPairCols + half * kCols;
       const bool mine = out.row0 < out.row_end && n0 < N;  // uniform over the warp
       const int row = min(out.row0 + lane, T - 1);
       if constexpr (kBlock) {
@@ -425,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // are added up, and the accumulator is released before the last are
           uint32_t r[2][16];
           if (mine) {
-            tmem_ld16(taddr + ab * BN, r[0]);
+            tmem_ld16(taddr + ab * kPairCols, r[0]);
             tmem_ld_wait();
           }
 #pragma unroll
@@ -433,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 1 == kCols / 16) {
               release(ab);
             } else if (mine) {
-              tmem_ld16(taddr + ab * BN + (c + 1) * 16, r[(c + 1) & 1]);
+              tmem_ld16(taddr + ab * kPairCols + (c + 1) * 16, r[(c + 1) & 1]);
             }
             if (mine) {
 #pragma unroll
@@ -467,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < kCols / 32; ++c) {
             uint32_t r[32];
-            tmem_ld32(taddr + ab * BN + c * 32, r);
+            tmem_ld32(taddr + ab * kPairCols + c * 32, r);
             tmem_ld_wait();
             float v[32];
 #pragma unroll
@@ -492,74 +466,562 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the peer's shared memory and TMEM stay live until the leader is done
+  cluster_sync();  // the peer's shared memory and TMEM stay live until the leader is done
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (CG == 2) {
-      tmem_dealloc_pair(tmem_base, 2 * BN);
-    } else {
-      tmem_dealloc(tmem_base, 2 * BN);
-    }
+    tmem_dealloc_pair(tmem_base, 2 * kPairCols);
   }
 }
 
-// Sets the kernel's shared-memory limit once per device; the clusters of CG
-// CTAs that can be resident at once (0: none, or a failed query).
-template <int CG, int BN, GScale SC, OutKind KIND>
-int gemm_capacity() {
-  static int cache[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  int &c = cache[dev & 63];
-  if (c == 0) {
-    auto kern = grouped_gemm_kernel<CG, BN, SC, KIND>;
-    constexpr uint32_t smem = GSmem<CG, BN>::kTotal;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
-    if (CG == 1) {
-      c = num_sms();
-    } else {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(CG, 1, 1);
-      cfg.blockDim = dim3(kThreads, 1, 1);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = CG;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
-      c = n;
-    }
+// Clusters of `size` CTAs of a kernel (one CTA per SM) that can be resident at
+// once, after raising its shared-memory limit; 0 if none or a query fails.
+int resident_clusters(const void *kern, int size, uint32_t smem) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
   }
-  return c;
-}
-
-template <int CG, int BN, GScale SC, OutKind KIND>
-cudaError_t run_gemm(const GroupedArgs &a, cudaStream_t st) {
-  constexpr int kRows = 128 * CG;
-  CUtensorMap tmA, tmB;
-  if (!make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
-  if (!make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, BN / CG)) return cudaErrorInvalidValue;
-  const int cap = gemm_capacity<CG, BN, SC, KIND>();
-  if (cap <= 0) return cudaErrorLaunchOutOfResources;
-  // at most one tile more per group than its rows alone would need
-  const int64_t groups = a.E < a.T ? a.E : a.T;
-  const int64_t most = (a.T / kRows + groups) * ((a.N + BN - 1) / BN);
-  const int units = (int)(most < cap ? most : cap);
-  return launch_pdl(grouped_gemm_kernel<CG, BN, SC, KIND>, dim3(units * CG), dim3(kThreads), GSmem<CG, BN>::kTotal, st,
-                    CG, tmA, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y), a.ldy, (int)a.T,
-                    (int)a.E, (int)a.N, (int)a.K, device_error_word());
+  if (size == 1) return num_sms();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
 }
 
 template <GScale SC, OutKind KIND>
+int pair_capacity() {
+  static int cache[64] = {};  // per device, capacity + 1
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int &c = cache[dev & 63];
+  if (c == 0)
+    c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_pair_kernel<SC, KIND>), 2, PairTileSmem::kTotal);
+  return c - 1;
+}
+
+template <GScale SC, OutKind KIND>
+cudaError_t run_pair(const GroupedArgs &a, cudaStream_t st) {
+  CUtensorMap tmA, tmB;
+  if (!make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
+  if (!make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, kPairCols / 2)) return cudaErrorInvalidValue;
+  // at most one tile more per group than its rows alone would need
+  const int64_t groups = a.E < a.T ? a.E : a.T;
+  const int64_t most = (a.T / kPairRows + groups) * ((a.N + kPairCols - 1) / kPairCols);
+  const int cap = pair_capacity<SC, KIND>(), units = (int)(most < cap ? most : cap);
+  return launch_pdl(grouped_pair_kernel<SC, KIND>, dim3(units * 2), dim3(kThreads), PairTileSmem::kTotal, st, 2, tmA,
+                    tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y), a.ldy, (int)a.T, (int)a.E,
+                    (int)a.N, (int)a.K, device_error_word());
+}
+
+// ---------------------------------------------------------------------------
+// Small groups, and too few tiles to fill the SMs evenly: 128 x 128 tiles, one
+// CTA each, whose K / 128 blocks are shared out too.  C clusters of S CTAs:
+// cluster c owns the tiles c, c + C, ... and its CTAs share their (tile,
+// block) items evenly, so a CTA holds the end of one tile, whole tiles, and
+// the beginning of another.  Split tiles' partial sums meet in shared memory:
+// every contributor adds up its share of the tile over all of them, in rank
+// order, so results do not depend on timing.  No workspace, no atomics.  Rows
+// of Xq are loaded 32 at a time, as many as the group has: the MMA's other
+// rows hold what the ring held before, and go nowhere.
+// ---------------------------------------------------------------------------
+constexpr int kMaxSplit = 8;  // CTAs per cluster
+
+struct SplitSmem {
+  static constexpr uint32_t kA = 128 * kBlk;
+  static constexpr uint32_t kB = 128 * kBlk;
+  static constexpr int kStages = 5;
+  static constexpr uint32_t kRing = kStages * (kA + kB);
+  static constexpr uint32_t kStaging = kEpiWarps * kStageBytes;
+  static constexpr uint32_t kTable = 2 * (kMaxExperts + 1) * 4 + 8;
+  static constexpr int kBufs = 3;  // accumulators in flight; a fourth parks one
+  static constexpr uint32_t kBars = (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static constexpr uint32_t kTotal = kRing + kStaging + kTable + kBars + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(2 * 128 * 128 * 4 <= kRing, "partial sums reuse the ring");
+};
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <OutKind KIND>
+__device__ __forceinline__ void put_four(uint8_t *y, int64_t i, const float (&v)[4]) {
+  if constexpr (KIND == OutKind::F32) {
+    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(y) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t p[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (KIND == OutKind::BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        p[k] = *reinterpret_cast<uint32_t *>(&h);
+      } else {
+        __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        p[k] = *reinterpret_cast<uint32_t *>(&h);
+      }
+    }
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(y) + i) = make_uint2(p[0], p[1]);
+  }
+}
+
+template <GScale SC, OutKind KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                         const __grid_constant__ CUtensorMap tmB, const float *__restrict__ x_scale,
+                         const float *__restrict__ w_scale, const int32_t *__restrict__ offsets,
+                         uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N, int K, int S, unsigned *err) {
+  using L = SplitSmem;
+  constexpr bool kF8 = SC != GScale::I8, kBlock = SC == GScale::Block;
+  constexpr int kBufs = L::kBufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sA = smem;
+  uint8_t *sB = smem + L::kStages * L::kA;
+  uint8_t *staging = smem + L::kRing;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + L::kStaging);
+  uint64_t *empty = full + L::kStages;
+  uint64_t *tfull = empty + L::kStages;
+  uint64_t *tempty = tfull + kBufs;
+  uint64_t *drain = tempty + kBufs;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  Groups g;
+  g.row = reinterpret_cast<int *>(tmem_slot + 4);
+  g.tile = g.row + kMaxExperts + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntn = (N + 127) / 128, nk = (K + kBlk - 1) / kBlk;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmA32);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // prologue done; the previous kernel's results are visible from here on
+  pdl_trigger();
+  build_groups(g, offsets, E, T, 128, ntn);
+
+  // this cluster's tiles c, c + C, ...; this CTA's items [w0, w1) of theirs
+  const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+  const int c = blockIdx.x / S, C = gridDim.x / S;
+  const int64_t items = (int64_t)max(0, (g.tile[E] - c + C - 1) / C) * nk;
+  const int64_t w0 = items * rank / S, w1 = items * (rank + 1) / S;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      uint32_t stage = 0, phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      Place p;
+      for (int64_t w = w0; w < w1 && ok;) {
+        const int lt = (int)(w / nk);
+        int kb = (int)(w % nk);
+        const int kend = (int)min((int64_t)nk, w1 - (int64_t)lt * nk);
+        p.find(g, E, c + lt * C, 128);
+        const int row_a = p.row0 + p.mb * 128, row_b = p.e * N + p.nb * 128;
+        const int boxes = min(4, (p.rows - p.mb * 128 + 31) / 32);  // 32 rows each
+        w += kend - kb;
+        for (; kb < kend; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], L::kB + boxes * 32 * kBlk);
+          tma_load_2d(&tmB, &full[stage], sB + stage * L::kB, kb * kBlk, row_b);
+          if (boxes == 4) {
+            tma_load_2d(&tmA, &full[stage], sA + stage * L::kA, kb * kBlk, row_a);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(&tmA32, &full[stage], sA + stage * L::kA + i * 32 * kBlk, kb * kBlk, row_a + i * 32);
+          }
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {  // let every issued copy land before the CTA may exit
+        for (int s = 0; s < L::kStages; ++s)
+          if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, nullptr, err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc = idesc8<kF8>(128, 128);
+      uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
+      bool ok = true;
+      int64_t seg = w0 + nk - w0 % nk;  // the tile's last item + 1
+      for (int64_t w = w0; w < w1; ++w) {
+        const bool first = kBlock || w == w0 || w == seg;
+        if (w == seg) seg += nk;
+        const bool last = kBlock || w + 1 == seg || w + 1 == w1;
+        if (first && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) break;
+        if (!mbar_wait(&full[stage], phase, abort_flag, err)) break;
+        tc_fence_after();
+        const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + stage * L::kA));
+        const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + stage * L::kB));
+#pragma unroll
+        for (int k = 0; k < kBlk / 32; ++k)
+          umma8<kF8>(tmem_base + ab * 128, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
+        umma_commit(&empty[stage]);
+        if (last) {
+          umma_commit(&tfull[ab]);
+          if (++ab == kBufs) {
+            ab = 0;
+            aphase ^= 1;
+          }
+        }
+        if (++stage == L::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every MMA issued above must finish before TMEM is released
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, err);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------- epilogue: a row per lane, 64 columns per warp ----------------
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    RowStore<KIND> out;
+    out.stage = staging + (warp - 4) * kStageBytes;
+    out.y = y;
+    out.ldy = ldy;
+    out.N = N;
+    out.lane = lane;
+    uint32_t ab = 0, aphase = 0;
+    bool ok = true, parked = false;
+    float2 acc[32];  // fp32 sums; for INT8 the bits of int32 sums
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+    Place p;
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[ab]);
+      if (++ab == kBufs) {
+        ab = 0;
+        aphase ^= 1;
+      }
+    };
+    for (int64_t w = w0; w < w1;) {
+      const int lt = (int)(w / nk), kb0 = (int)(w % nk);
+      const int kend = (int)min((int64_t)nk, w1 - (int64_t)lt * nk);
+      p.find(g, E, c + lt * C, 128);
+      out.row0 = p.row0 + p.mb * 128 + quarter * 32;
+      out.row_end = p.row0 + p.rows;
+      const int n0 = p.nb * 128 + half * 64;
+      const bool mine = out.row0 < out.row_end && n0 < N;  // uniform over the warp
+      const int row = min(out.row0 + lane, T - 1);
+      w += kend - kb0;
+      if constexpr (kBlock) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        const float *xs = x_scale + (int64_t)row * nk;
+        const float *ws = w_scale + ((int64_t)p.e * ntn + p.nb) * nk;
+        float s = __fmul_rn(__ldg(xs + kb0), __ldg(ws + kb0));
+        for (int kb = kb0; kb < kend; ++kb) {
+          const int kn = min(kb + 1, nk - 1);
+          const float xn = __ldg(xs + kn), wn = __ldg(ws + kn);  // the next block's scales
+          ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], aphase, abort_flag, err));
+          if (!ok) break;
+          tc_fence_after();
+          const float2 s2 = make_float2(s, s);
+          const uint32_t src = taddr + ab * 128;
+          // columns 16 at a time: the next ones are on their way while these
+          // are added up, and the accumulator is released before the last are
+          uint32_t r[2][16];
+          if (mine) {
+            tmem_ld16(src, r[0]);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q == 3) {
+              release();
+            } else if (mine) {
+              tmem_ld16(src + (q + 1) * 16, r[(q + 1) & 1]);
+            }
+            if (mine) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                acc[q * 8 + j] = ffma2_rn(
+                    make_float2(__uint_as_float(r[q & 1][2 * j]), __uint_as_float(r[q & 1][2 * j + 1])), s2,
+                    acc[q * 8 + j]);
+              if (q < 3) tmem_ld_wait();
+            }
+          }
+          s = __fmul_rn(xn, wn);
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], aphase, abort_flag, err));
+        if (ok) {
+          tc_fence_after();
+          if (mine) {
+            uint32_t r[2][32];
+            tmem_ld32(taddr + ab * 128, r[0]);
+            tmem_ld32(taddr + ab * 128 + 32, r[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              acc[j] = make_float2(__uint_as_float(r[j / 16][2 * (j % 16)]), __uint_as_float(r[j / 16][2 * (j % 16) + 1]));
+          }
+          release();
+        }
+      }
+      if (!ok) break;
+      if (kb0 == 0 && kend == nk) {  // a whole tile
+        if (mine) {
+          const float dx = kBlock ? 0.0f : __ldg(x_scale + row);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              v[2 * j] = acc[h * 16 + j].x;
+              v[2 * j + 1] = acc[h * 16 + j].y;
+            }
+            if constexpr (!kBlock) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int n = n0 + h * 32 + j * 4;
+                const float4 dw = n < N ? __ldg(reinterpret_cast<const float4 *>(w_scale + (int64_t)p.e * N + n))
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[4 * j] = __fmul_rn(__fmul_rn(acc_value<kF8>(__float_as_uint(v[4 * j])), dx), dw.x);
+                v[4 * j + 1] = __fmul_rn(__fmul_rn(acc_value<kF8>(__float_as_uint(v[4 * j + 1])), dx), dw.y);
+                v[4 * j + 2] = __fmul_rn(__fmul_rn(acc_value<kF8>(__float_as_uint(v[4 * j + 2])), dx), dw.z);
+                v[4 * j + 3] = __fmul_rn(__fmul_rn(acc_value<kF8>(__float_as_uint(v[4 * j + 3])), dx), dw.w);
+              }
+            }
+            out.put(v, n0 + h * 32);
+          }
+        }
+      } else if (w < w1) {  // the end of a tile begun by an earlier CTA, with more to come: parked in TMEM
+        parked = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            r[2 * j] = __float_as_uint(acc[q * 8 + j].x);
+            r[2 * j + 1] = __float_as_uint(acc[q * 8 + j].y);
+          }
+          tmem_st16(taddr + kBufs * 128 + q * 16, r);
+        }
+        tmem_st_wait();
+      }
+    }
+    if (S > 1 && ok) {
+      // partial sums into the ring, which no load or MMA uses any more:
+      // [slot][row of the tile][channel], slot 0 for a tile begun by an
+      // earlier CTA, slot 1 for one that a later CTA ends; 16-byte chunks
+      // swizzled by row
+      const int r = quarter * 32 + lane;
+      uint4 *mine4 = reinterpret_cast<uint4 *>(smem) + r * 32;
+      const bool one = w0 / nk == (w1 - 1) / nk;  // the CTA's items are of one tile
+      if (w1 > w0 && (w1 % nk != 0 || (one && w0 % nk != 0))) {
+        uint4 *d = mine4 + (one && w0 % nk != 0 ? 0 : 128 * 32);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          d[(half * 16 + j) ^ (r & 7)] = make_uint4(__float_as_uint(acc[2 * j].x), __float_as_uint(acc[2 * j].y),
+                                                    __float_as_uint(acc[2 * j + 1].x), __float_as_uint(acc[2 * j + 1].y));
+      }
+      if (parked) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[16];
+          tmem_ld16(taddr + kBufs * 128 + q * 16, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mine4[(half * 16 + q * 4 + j) ^ (r & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (S > 1) {
+    cluster_sync();  // every CTA's partial sums are written
+    if (w1 > w0) {
+      Place p;
+#pragma unroll 1
+      for (int slot = 0; slot < 2; ++slot) {
+        // the split tile, if there is one
+        const int lt = (int)(slot == 0 ? w0 / nk : (w1 - 1) / nk);
+        const int64_t i0 = (int64_t)lt * nk, i1 = i0 + nk;
+        if (slot == 0 ? i0 == w0 : (i0 < w0 || i1 <= w1)) continue;
+        // its contributors: the CTAs with its first to its last item
+        const int ra = (int)(((i0 + 1) * S - 1) / items), rb = (int)((i1 * S - 1) / items), cnt = rb - ra + 1;
+        p.find(g, E, c + lt * C, 128);
+        const int rows = min(128, p.rows - p.mb * 128), row = p.row0 + p.mb * 128;
+        const int u1 = rows * 32 * (rank - ra + 1) / cnt;  // four channels of one row each
+        for (int u = rows * 32 * (rank - ra) / cnt + threadIdx.x; u < u1; u += kThreads) {
+          const int t = u >> 5, n = p.nb * 128 + (u & 31) * 4;
+          const uint32_t at = smem_u32(smem) + (uint32_t)(t * 32 + ((u & 31) ^ (t & 7))) * 16;
+          uint32_t part[kMaxSplit][4];
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q)
+            if (q < cnt) {  // the first contributor began the tile: its slot 1
+              const uint4 v = ld_shared_cluster_v4(mapa_shared(at + (q == 0 ? 128 * 128 * 4 : 0), ra + q));
+              part[q][0] = v.x;
+              part[q][1] = v.y;
+              part[q][2] = v.z;
+              part[q][3] = v.w;
+            }
+          if (n < N) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t sum = part[0][k];
+#pragma unroll
+              for (int q = 1; q < kMaxSplit; ++q)
+                if (q < cnt) {
+                  if constexpr (kF8) {
+                    sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(part[q][k])));
+                  } else {
+                    sum += part[q][k];
+                  }
+                }
+              v[k] = acc_value<kF8>(sum);
+              if constexpr (!kBlock)
+                v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row + t)), __ldg(w_scale + (int64_t)p.e * N + n + k));
+            }
+            put_four<KIND>(y, (int64_t)(row + t) * ldy + n, v);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while a peer still reads its partial sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+}
+
+template <GScale SC, OutKind KIND>
+int split_capacity(int S) {
+  static int cache[64][kMaxSplit + 1] = {};  // per device and size, capacity + 1
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int &c = cache[dev & 63][S];
+  if (c == 0)
+    c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_split_kernel<SC, KIND>), S, SplitSmem::kTotal);
+  return c - 1;
+}
+
+// How the split kernel is laid over the SMs: C clusters of S CTAs, and the
+// blocks that the busiest CTA gets (cost).
+struct SplitPlan {
+  int S = 0, C = 0;
+  int64_t cost = INT64_MAX;
+};
+
+// The split with the least cost.  One that splits tiles pays about 14 blocks
+// for its two cluster barriers and the partial sums (4096 x 4096 at 128 rows:
+// 18.0 us unsplit, 14.9, 12.9 and 11.7 us with S = 2, 3 and 4).  Every CTA of a
+// split cluster gets items (nk >= S), so that a tile's contributors are
+// consecutive.
+template <GScale SC, OutKind KIND>
+SplitPlan plan_split(int64_t tiles, int64_t nk) {
+  SplitPlan best;
+  for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
+    const int64_t cap = split_capacity<SC, KIND>(S), C = tiles < cap ? tiles : cap;
+    if (C <= 0) continue;
+    const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 14 : 0);
+    if (cost < best.cost) {
+      best.S = S;
+      best.C = (int)C;
+      best.cost = cost;
+    }
+  }
+  return best;
+}
+
+template <GScale SC, OutKind KIND>
+cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t st) {
+  CUtensorMap tmA, tmA32, tmB;
+  if (!make_code_tmap(&tmA, a.xq, a.T, a.K, 128) || !make_code_tmap(&tmA32, a.xq, a.T, a.K, 32) ||
+      !make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, 128))
+    return cudaErrorInvalidValue;
+  return launch_pdl(grouped_split_kernel<SC, KIND>, dim3(plan.C * plan.S), dim3(kThreads), SplitSmem::kTotal, st,
+                    (unsigned)plan.S, tmA, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
+                    a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, plan.S, device_error_word());
+}
+
+// Row tiles of `rows` rows each over all groups.  The groups' sizes are on the
+// device: the host reckons with rows spread evenly over as many groups as can
+// have any, and half a tile of each group's last one empty.
+int64_t row_tiles(const GroupedArgs &a, int64_t rows) {
+  if (a.offsets == nullptr) return (a.T + rows - 1) / rows;
+  const int64_t groups = a.E < a.T ? a.E : a.T;
+  const int64_t spread = (2 * a.T + groups * rows) / (2 * rows);
+  return spread > groups ? spread : groups;
+}
+
+// Pairs on 256 x 256 tiles or single CTAs on 128 x 128 ones: whichever's
+// busiest unit has less to do.  A block of a pair's tile takes 1.2 times as
+// long as one of a single's (block scales: 1.4 times, their sums waiting on
+// both CTAs), for four times the products; measured at 512 to 24576 rows.
+template <GScale SC, OutKind KIND>
 cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
-  // pairs once 256 x 256 tiles occupy every pair and groups fill their rows
-  const int64_t tiles = (a.T + 255) / 256 * ((a.N + 255) / 256);
-  if (a.T / a.E >= 128 && tiles >= num_sms() / 2) return run_gemm<2, 256, SC, KIND>(a, st);
-  return run_gemm<1, 128, SC, KIND>(a, st);
+  const int64_t nk = (a.K + kBlk - 1) / kBlk;
+  const SplitPlan split = plan_split<SC, KIND>(row_tiles(a, 128) * ((a.N + 127) / 128), nk);
+  const int64_t cap = pair_capacity<SC, KIND>();
+  if (cap > 0) {
+    const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
+    const int64_t blocks = (tiles + cap - 1) / cap * nk;
+    if (split.S == 0 || blocks * (SC == GScale::Block ? 14 : 12) < split.cost * 10) return run_pair<SC, KIND>(a, st);
+  }
+  if (split.S == 0) return cudaErrorLaunchOutOfResources;
+  return run_split<SC, KIND>(a, split, st);
 }
 
 template <GScale SC>
