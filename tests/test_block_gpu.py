@@ -262,3 +262,51 @@ def test_block_calls_on_another_stream_and_in_a_graph():
     y = chain()
     assert torch.equal(y, y3)
     assert sq.sq_check_device_error() == sq.SQ_OK
+
+
+def _e4m3_midpoints():
+    v = oracle.e4m3_decode(np.arange(256, dtype=np.uint8)).astype(np.float64)
+    v = np.unique(np.abs(v[~np.isnan(v)]))
+    return (v[1:] + v[:-1]) / 2
+
+
+@pytest.mark.parametrize("kind", ["bf16_ties", "few_bits", "next_to_few_bits", "small"])
+def test_codes_next_to_e4m3_midpoints(kind):
+    # values within a few ulps of (E4M3 midpoint) * scale.  Scales: of bf16
+    # maxima (exact ties), of four significant bits, within 20 ulps of those
+    # (where only a division decides), and around 2^-90 and 2^-126
+    rng = np.random.default_rng(7)
+    R, K = 256, 512
+    mids = _e4m3_midpoints()
+    x = np.zeros((R, K), np.float32)
+    for r in range(R):
+        for b in range(K // B):
+            if kind == "bf16_ties":
+                d = rng.integers(128, 256) * 2.0 ** rng.integers(-12, 4) / 448.0
+            elif kind == "small":
+                d = rng.uniform(1, 2) * 2.0 ** rng.choice([-91, -90, -89, -125, -126, -127, -140])
+            else:
+                d = rng.integers(8, 16) / 8.0 * 2.0 ** rng.integers(-12, 4)
+                if kind == "next_to_few_bits":
+                    d *= 1 + rng.integers(-20, 21) * 2.0 ** -23
+            m = np.float32(448.0 * d)
+            d = np.float64(m / np.float32(448.0))
+            v = (rng.choice(mids, B) * d).astype(np.float32)
+            v = (v.view(np.int32) + np.where(v > 1e-37, rng.integers(-2, 3, B), 0).astype(np.int32)).view(np.float32)
+            v *= rng.choice([-1, 1], B)
+            v[rng.integers(0, B, 4)] = -0.0
+            v = np.clip(v, -m, m)
+            v[0] = m
+            x[r, b * B:(b + 1) * B] = v
+    t = torch.from_numpy(x)
+    if kind == "bf16_ties":
+        t = t.to(torch.bfloat16)
+        x = t.float().numpy()
+    q, s = sq.sq_quant_act_e4m3_block(t.to(DEV))
+    q_ref, s_ref = oracle_rows(x)
+    np.testing.assert_array_equal(s.cpu().numpy(), s_ref)
+    np.testing.assert_array_equal(q.cpu().numpy(), q_ref)
+    q, s, _, _ = sq.sq_smooth_quant_weight_e4m3_block(t.to(DEV))
+    q_ref, s_ref = oracle_weight(x[None])
+    np.testing.assert_array_equal(s.cpu().numpy(), s_ref[0])
+    np.testing.assert_array_equal(q.cpu().numpy(), q_ref[0])
