@@ -449,41 +449,49 @@ def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> None:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _on_stream(device, stream, call):
-    """call(stream handle) with `device` current and allocations on the stream."""
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.index != torch._C._cuda_getDevice()
+
+
+def _at(device, stream):
+    """Context in which `device` and the stream to launch on are current."""
     if stream is None:
-        # the handle alone: building torch's stream object costs more than a launch
-        index = device.index
-        if index == torch._C._cuda_getDevice():
-            return call(torch._C._cuda_getCurrentRawStream(index))
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return torch.cuda.device(device)
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _handle(device) -> int:
+    """The current stream's handle (torch's stream object costs more to build than a launch)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def sq_quant_act_e4m3_block(x: torch.Tensor, inv_smooth=None, xq=None, x_scale=None, stream=None):
     """(xq [M,K] uint8 E4M3, x_scale [M, ceil(K/128)] = absmax/448 per token and
     128 channels) of x * inv_smooth (None: of x)."""
     _rowmajor(x, "x")
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return sq_quant_act_e4m3_block(x, inv_smooth, xq, x_scale)
     M, K = x.shape
-    dt, dev = _dtype(x, "x"), x.device
+    dt, KB = _dtype(x, "x"), _blocks(K)
     if inv_smooth is not None:
         _expect(inv_smooth, "inv_smooth", torch.float32, (K,), dev)
-    if xq is not None:
+    if xq is None:
+        xq = x.new_empty((M, K), dtype=torch.uint8)
+    else:
         _expect(xq, "xq", torch.uint8, (M, K), dev)
-    if x_scale is not None:
-        _expect(x_scale, "x_scale", torch.float32, (M, _blocks(K)), dev)
-
-    def call(st):
-        q = torch.empty((M, K), dtype=torch.uint8, device=dev) if xq is None else xq
-        s = torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev) if x_scale is None else x_scale
-        _check(lib().sq_quant_act_e4m3_block(x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K,
-                                             None if inv_smooth is None else inv_smooth.data_ptr(), q.data_ptr(),
-                                             s.data_ptr(), st), "sq_quant_act_e4m3_block")
-        return q, s
-    return _on_stream(dev, stream, call)
+    if x_scale is None:
+        x_scale = x.new_empty((M, KB), dtype=torch.float32)
+    else:
+        _expect(x_scale, "x_scale", torch.float32, (M, KB), dev)
+    _check(lib().sq_quant_act_e4m3_block(x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K,
+                                         None if inv_smooth is None else inv_smooth.data_ptr(), xq.data_ptr(),
+                                         x_scale.data_ptr(), _handle(dev)), "sq_quant_act_e4m3_block")
+    return xq, x_scale
 
 
 def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float = 0.5, wq=None, w_scale=None,
@@ -497,47 +505,50 @@ def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float =
         raise ValueError("w must be a 2-D or 3-D tensor with unit column stride")
     if not w.is_cuda:
         raise ValueError("w must be on a CUDA device")
+    dev = w.device
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return sq_smooth_quant_weight_e4m3_block(w, amax, alpha, wq, w_scale, smooth, inv_smooth)
     E, (N, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
     ldw = w.stride(-2) if N > 1 else (w.stride(0) if w.dim() == 3 and E > 1 else K)
     if w.dim() == 3 and E > 1 and w.stride(0) != N * ldw:
         raise ValueError("w's experts must follow one another (stride(0) == N * stride(1))")
-    dt, dev = _dtype(w, "w"), w.device
+    dt = _dtype(w, "w")
     scale_shape = (*w.shape[:-2], _blocks(N), _blocks(K))
-    if wq is not None:
-        _expect(wq, "wq", torch.uint8, w.shape, dev)
-    if w_scale is not None:
-        _expect(w_scale, "w_scale", torch.float32, scale_shape, dev)
     for t, name in ((amax, "amax"), (smooth, "smooth"), (inv_smooth, "inv_smooth")):
         if t is not None:
             _expect(t, name, torch.float32, (K,), dev)
+    if wq is None:
+        wq = w.new_empty(w.shape, dtype=torch.uint8)
+    else:
+        _expect(wq, "wq", torch.uint8, w.shape, dev)
+    if w_scale is None:
+        w_scale = w.new_empty(scale_shape, dtype=torch.float32)
+    else:
+        _expect(w_scale, "w_scale", torch.float32, scale_shape, dev)
+    if amax is not None:
+        smooth = torch.empty_like(amax) if smooth is None else smooth
+        inv_smooth = torch.empty_like(amax) if inv_smooth is None else inv_smooth
+    _check(lib().sq_smooth_quant_weight_e4m3_block(
+        w.data_ptr(), dt, E, N, K, ldw, None if amax is None else amax.data_ptr(), alpha, wq.data_ptr(),
+        w_scale.data_ptr(), None if smooth is None else smooth.data_ptr(),
+        None if inv_smooth is None else inv_smooth.data_ptr(), _handle(dev)), "sq_smooth_quant_weight_e4m3_block")
+    return wq, w_scale, smooth, inv_smooth
 
-    def call(st):
-        q = torch.empty(w.shape, dtype=torch.uint8, device=dev) if wq is None else wq
-        sc = torch.empty(scale_shape, dtype=torch.float32, device=dev) if w_scale is None else w_scale
-        s, inv = smooth, inv_smooth
-        if amax is not None:
-            s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else s
-            inv = torch.empty(K, dtype=torch.float32, device=dev) if inv is None else inv
-        _check(lib().sq_smooth_quant_weight_e4m3_block(_ptr(w), dt, E, N, K, ldw, _ptr(amax), ctypes.c_float(alpha),
-                                                       _ptr(q), _ptr(sc), _ptr(s), _ptr(inv), st),
-               "sq_smooth_quant_weight_e4m3_block")
-        return q, sc, s, inv
-    return _on_stream(dev, stream, call)
 
-
-def _out_matrix(y, T: int, N: int, out_dtype, dev):
-    """y checked, or None for one that the caller allocates; the output type."""
+def _out_matrix(x: torch.Tensor, y, T: int, N: int, out_dtype) -> torch.Tensor:
+    """y checked, or a new [T, N] matrix of out_dtype beside x."""
     if y is None:
         if out_dtype not in _DT:
             raise ValueError(f"out_dtype {out_dtype} not supported (float32/float16/bfloat16)")
-        return out_dtype
+        return x.new_empty((T, N), dtype=out_dtype)
     _rowmajor(y, "y")
     _dtype(y, "y")
     if y.shape != (T, N):
         raise ValueError(f"y must have shape {(T, N)}, not {tuple(y.shape)}")
-    if y.device != dev:
-        raise ValueError(f"y must be on {dev}, not {y.device}")
-    return y.dtype
+    if y.device != x.device:
+        raise ValueError(f"y must be on {x.device}, not {y.device}")
+    return y
 
 
 def sq_w8a8_linear_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
@@ -545,43 +556,43 @@ def sq_w8a8_linear_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch
     """y [M,N] = dequantized xq times dequantized wq^T for block-scaled E4M3
     codes: x_scale [M, ceil(K/128)], w_scale [ceil(N/128), ceil(K/128)]."""
     _rowmajor(xq, "xq")
+    dev = xq.device
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return sq_w8a8_linear_e4m3_block(xq, x_scale, wq, w_scale, out_dtype, y)
     M, K = xq.shape
-    N, dev = wq.shape[0], xq.device
+    N, KB = wq.shape[0], _blocks(K)
     _expect(xq, "xq", torch.uint8, (M, K), dev)
     _expect(wq, "wq", torch.uint8, (N, K), dev)
-    _expect(x_scale, "x_scale", torch.float32, (M, _blocks(K)), dev)
-    _expect(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
-    dt = _out_matrix(y, M, N, out_dtype, dev)
-
-    def call(st):
-        out = torch.empty((M, N), dtype=dt, device=dev) if y is None else y
-        _check(lib().sq_w8a8_linear_e4m3_block(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-                                               M, N, K, out.data_ptr(), _DT[dt], out.stride(0) if M > 1 else N, st),
-               "sq_w8a8_linear_e4m3_block")
-        return out
-    return _on_stream(dev, stream, call)
+    _expect(x_scale, "x_scale", torch.float32, (M, KB), dev)
+    _expect(w_scale, "w_scale", torch.float32, (_blocks(N), KB), dev)
+    y = _out_matrix(xq, y, M, N, out_dtype)
+    _check(lib().sq_w8a8_linear_e4m3_block(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                                           M, N, K, y.data_ptr(), _DT[y.dtype], y.stride(0) if M > 1 else N,
+                                           _handle(dev)), "sq_w8a8_linear_e4m3_block")
+    return y
 
 
 def _grouped(name: str, code_dtype, block: bool, xq, x_scale, wq, w_scale, offsets, out_dtype, y, stream):
     _rowmajor(xq, "xq")
+    dev = xq.device
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return _grouped(name, code_dtype, block, xq, x_scale, wq, w_scale, offsets, out_dtype, y, None)
     if wq.dim() != 3:
         raise ValueError("wq must be a 3-D tensor [E, N, K]")
     T, K = xq.shape
-    E, N, dev = wq.shape[0], wq.shape[1], xq.device
+    E, N, _ = wq.shape
     _expect(xq, "xq", code_dtype, (T, K), dev)
     _expect(wq, "wq", code_dtype, (E, N, K), dev)
     _expect(x_scale, "x_scale", torch.float32, (T, _blocks(K)) if block else (T,), dev)
     _expect(w_scale, "w_scale", torch.float32, (E, _blocks(N), _blocks(K)) if block else (E, N), dev)
     _expect(offsets, "offsets", torch.int32, (E + 1,), dev)
-    dt = _out_matrix(y, T, N, out_dtype, dev)
-
-    def call(st):
-        out = torch.empty((T, N), dtype=dt, device=dev) if y is None else y
-        _check(getattr(lib(), name)(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-                                    offsets.data_ptr(), T, E, N, K, out.data_ptr(), _DT[dt],
-                                    out.stride(0) if T > 1 else N, st), name)
-        return out
-    return _on_stream(dev, stream, call)
+    y = _out_matrix(xq, y, T, N, out_dtype)
+    _check(getattr(lib(), name)(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+                                offsets.data_ptr(), T, E, N, K, y.data_ptr(), _DT[y.dtype],
+                                y.stride(0) if T > 1 else N, _handle(dev)), name)
+    return y
 
 
 def sq_w8a8_linear_grouped(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,

@@ -501,10 +501,8 @@ int resident_clusters(const void *kern, int size, uint32_t smem) {
 }
 
 template <GScale SC, OutKind KIND>
-int pair_capacity() {
+int pair_capacity(int dev) {
   static int cache[64] = {};  // per device, capacity + 1
-  int dev = 0;
-  cudaGetDevice(&dev);
   int &c = cache[dev & 63];
   if (c == 0)
     c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_pair_kernel<SC, KIND>), 2, PairTileSmem::kTotal);
@@ -512,14 +510,14 @@ int pair_capacity() {
 }
 
 template <GScale SC, OutKind KIND>
-cudaError_t run_pair(const GroupedArgs &a, cudaStream_t st) {
+cudaError_t run_pair(const GroupedArgs &a, int cap, cudaStream_t st) {
   CUtensorMap tmA, tmB;
   if (!make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
   if (!make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, kPairCols / 2)) return cudaErrorInvalidValue;
   // at most one tile more per group than its rows alone would need
   const int64_t groups = a.E < a.T ? a.E : a.T;
   const int64_t most = (a.T / kPairRows + groups) * ((a.N + kPairCols - 1) / kPairCols);
-  const int cap = pair_capacity<SC, KIND>(), units = (int)(most < cap ? most : cap);
+  const int units = (int)(most < cap ? most : cap);
   return launch_pdl(grouped_pair_kernel<SC, KIND>, dim3(units * 2), dim3(kThreads), PairTileSmem::kTotal, st, 2, tmA,
                     tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y), a.ldy, (int)a.T, (int)a.E,
                     (int)a.N, (int)a.K, device_error_word());
@@ -947,10 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <GScale SC, OutKind KIND>
-int split_capacity(int S) {
+int split_capacity(int dev, int S) {
   static int cache[64][kMaxSplit + 1] = {};  // per device and size, capacity + 1
-  int dev = 0;
-  cudaGetDevice(&dev);
   int &c = cache[dev & 63][S];
   if (c == 0)
     c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_split_kernel<SC, KIND>), S, SplitSmem::kTotal);
@@ -970,10 +966,10 @@ struct SplitPlan {
 // split cluster gets items (nk >= S), so that a tile's contributors are
 // consecutive.
 template <GScale SC, OutKind KIND>
-SplitPlan plan_split(int64_t tiles, int64_t nk) {
+SplitPlan plan_split(int dev, int64_t tiles, int64_t nk) {
   SplitPlan best;
   for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
-    const int64_t cap = split_capacity<SC, KIND>(S), C = tiles < cap ? tiles : cap;
+    const int64_t cap = split_capacity<SC, KIND>(dev, S), C = tiles < cap ? tiles : cap;
     if (C <= 0) continue;
     const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 14 : 0);
     if (cost < best.cost) {
@@ -988,9 +984,11 @@ SplitPlan plan_split(int64_t tiles, int64_t nk) {
 template <GScale SC, OutKind KIND>
 cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t st) {
   CUtensorMap tmA, tmA32, tmB;
-  if (!make_code_tmap(&tmA, a.xq, a.T, a.K, 128) || !make_code_tmap(&tmA32, a.xq, a.T, a.K, 32) ||
-      !make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, 128))
+  if (!make_code_tmap(&tmA32, a.xq, a.T, a.K, 32) || !make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, 128))
     return cudaErrorInvalidValue;
+  tmA = tmA32;
+  // (a tile of no more than 96 rows is loaded by 32)
+  if (a.T > 96 && !make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
   return launch_pdl(grouped_split_kernel<SC, KIND>, dim3(plan.C * plan.S), dim3(kThreads), SplitSmem::kTotal, st,
                     (unsigned)plan.S, tmA, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
                     a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, plan.S, device_error_word());
@@ -1013,12 +1011,15 @@ int64_t row_tiles(const GroupedArgs &a, int64_t rows) {
 template <GScale SC, OutKind KIND>
 cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   const int64_t nk = (a.K + kBlk - 1) / kBlk;
-  const SplitPlan split = plan_split<SC, KIND>(row_tiles(a, 128) * ((a.N + 127) / 128), nk);
-  const int64_t cap = pair_capacity<SC, KIND>();
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const SplitPlan split = plan_split<SC, KIND>(dev, row_tiles(a, 128) * ((a.N + 127) / 128), nk);
+  const int cap = pair_capacity<SC, KIND>(dev);
   if (cap > 0) {
     const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
     const int64_t blocks = (tiles + cap - 1) / cap * nk;
-    if (split.S == 0 || blocks * (SC == GScale::Block ? 14 : 12) < split.cost * 10) return run_pair<SC, KIND>(a, st);
+    if (split.S == 0 || blocks * (SC == GScale::Block ? 14 : 12) < split.cost * 10) return run_pair<SC, KIND>(a, cap, st);
   }
   if (split.S == 0) return cudaErrorLaunchOutOfResources;
   return run_split<SC, KIND>(a, split, st);
