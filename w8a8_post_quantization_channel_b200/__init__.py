@@ -481,11 +481,11 @@ def sq_quant_act_e4m3_block(x: torch.Tensor, inv_smooth=None, xq=None, x_scale=N
     if inv_smooth is not None:
         _expect(inv_smooth, "inv_smooth", torch.float32, (K,), dev)
     if xq is None:
-        xq = x.new_empty((M, K), dtype=torch.uint8)
+        xq = torch.empty(M, K, dtype=torch.uint8, device=dev)
     else:
         _expect(xq, "xq", torch.uint8, (M, K), dev)
     if x_scale is None:
-        x_scale = x.new_empty((M, KB), dtype=torch.float32)
+        x_scale = torch.empty(M, KB, dtype=torch.float32, device=dev)
     else:
         _expect(x_scale, "x_scale", torch.float32, (M, KB), dev)
     _check(lib().sq_quant_act_e4m3_block(x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K,
@@ -519,11 +519,11 @@ def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float =
         if t is not None:
             _expect(t, name, torch.float32, (K,), dev)
     if wq is None:
-        wq = w.new_empty(w.shape, dtype=torch.uint8)
+        wq = torch.empty(*w.shape, dtype=torch.uint8, device=dev)
     else:
         _expect(wq, "wq", torch.uint8, w.shape, dev)
     if w_scale is None:
-        w_scale = w.new_empty(scale_shape, dtype=torch.float32)
+        w_scale = torch.empty(*scale_shape, dtype=torch.float32, device=dev)
     else:
         _expect(w_scale, "w_scale", torch.float32, scale_shape, dev)
     if amax is not None:
@@ -541,7 +541,7 @@ def _out_matrix(x: torch.Tensor, y, T: int, N: int, out_dtype) -> torch.Tensor:
     if y is None:
         if out_dtype not in _DT:
             raise ValueError(f"out_dtype {out_dtype} not supported (float32/float16/bfloat16)")
-        return x.new_empty((T, N), dtype=out_dtype)
+        return torch.empty(T, N, dtype=out_dtype, device=x.device)
     _rowmajor(y, "y")
     _dtype(y, "y")
     if y.shape != (T, N):
