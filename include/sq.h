@@ -402,9 +402,10 @@ sq_status sq_w8a8_linear_e4m3_block(const uint8_t *xq, const float *x_scale,
  *   [E][NB][KB], each group's rows within sq_w8a8_linear_e4m3_block's bound.
  * The E4M3 sums' order depends on T, E, N, K and the offsets alone: the same
  * bits on every call.
- * T == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N, E * N < 2^31;
- * E <= 1024, else SQ_ERR_UNSUPPORTED.  offsets is 4-byte aligned.  No
- * workspace.
+ * T == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N, E * N < 2^31.
+ * E <= 1024, T <= 2^31 - 1024 and fewer than 2^31 tiles of 128 x 128 in Y,
+ * else SQ_ERR_UNSUPPORTED (the last two for sq_w8a8_linear_e4m3_block too).
+ * offsets is 4-byte aligned.  No workspace.
  */
 sq_status sq_w8a8_linear_grouped(const int8_t *xq, const float *x_scale,
                                  const int8_t *wq, const float *w_scale,

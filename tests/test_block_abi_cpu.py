@@ -52,6 +52,7 @@ def test_linear_block():
                 dict(ws=MIS), dict(M=-1), dict(M=1 << 31), dict(N=40), dict(N=0), dict(K=40), dict(K=0), dict(y=None),
                 dict(y=MIS), dict(yt=9), dict(ldy=128), dict(ldy=257)):
         assert call(**bad) == INV, bad
+    assert call(M=(1 << 31) - 1023) == UNS
 
 
 @pytest.mark.parametrize("name", ["sq_w8a8_linear_grouped", "sq_w8a8_linear_grouped_e4m3",
@@ -68,7 +69,8 @@ def test_grouped(name):
                 dict(ldy=128), dict(ldy=257)):
         assert call(**bad) == INV, bad
     assert call(E=1025) == UNS
-    assert call(T=(1 << 31) - 16, N=1 << 20, ldy=1 << 20) == UNS      # more tiles than are numbered in 32 bits
+    assert call(T=(1 << 31) - 2048, N=1 << 20, ldy=1 << 20) == UNS    # more tiles than are numbered in 32 bits
+    assert call(T=(1 << 31) - 1023) == UNS                            # a tile's last rows pass 2^31
 
 
 def test_binding_refuses_what_it_cannot_pass_on():

@@ -6,6 +6,10 @@ sum bit for bit.  E4M3: within the fp32 accumulator's bound of the dense call
 (2^-24 each).  Block scales: the bound of the dense block-scaled linear.
 Rounding to the output type adds half a step.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -139,6 +143,17 @@ def test_offsets_out_of_order_stay_inside(scale, T):
     assert sq.sq_check_device_error() == sq.SQ_OK
 
 
+@pytest.mark.parametrize("scale", ["i8", "block"])
+@pytest.mark.parametrize("T,E,K", [(5, 3, 1024), (500, 2, 4096)])
+def test_no_rows_in_any_group(scale, T, E, K):
+    ops = codes(T, E, 272, K, scale, seed=6)
+    y = torch.full((T, 272), 5.0, dtype=torch.bfloat16, device=DEV)
+    for first in (0, T // 2, T):
+        CALL[scale](*ops, torch.full((E + 1,), first, dtype=torch.int32, device=DEV), y=y)
+    assert torch.all(y == 5.0)
+    assert sq.sq_check_device_error() == sq.SQ_OK
+
+
 def test_int8_groups_equal_the_dense_call():
     N, K, sizes = 528, 1040, [70, 1, 0, 200, 33]
     xq, xs, wq, ws = codes(sum(sizes), len(sizes), N, K, "i8", seed=4)
@@ -179,6 +194,33 @@ def test_one_graph_serves_changing_groups_and_streams(scale):
     torch.cuda.current_stream().wait_stream(side)
     check(y, *ops, off, scale, "bf16")
     assert sq.sq_check_device_error() == sq.SQ_OK
+
+
+def test_first_call_of_a_process_is_captured():
+    # nothing that a call sets up on first use may need to run outside a capture
+    code = """
+import torch
+import w8a8_post_quantization_channel_b200 as sq
+x = torch.randn(40, 528, device="cuda")
+w = torch.randn(3, 272, 528, device="cuda")
+off = torch.tensor([0, 7, 7, 40], dtype=torch.int32, device="cuda")
+def run():
+    q, s = sq.sq_quant_act_e4m3_block(x)
+    wq, ws, _, _ = sq.sq_smooth_quant_weight_e4m3_block(w)
+    return sq.sq_w8a8_linear_grouped_e4m3_block(q, s, wq, ws, off, torch.float32)
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    y = run()
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, run())
+assert sq.sq_check_device_error() == sq.SQ_OK
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_outputs_past_two_gib_elements():
