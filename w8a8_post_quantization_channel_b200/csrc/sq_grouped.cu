@@ -536,6 +536,12 @@ cudaError_t run_pair(const GroupedArgs &a, int cap, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplit = 8;  // CTAs per cluster
 
+// A split tile that this CTA helps to add up: cnt contributors from rank ra on
+// (0: there is none), its expert, first row, rows and first channel.
+struct SplitTile {
+  int cnt, ra, e, row, rows, n;
+};
+
 struct SplitSmem {
   static constexpr uint32_t kA = 128 * kBlk;
   static constexpr uint32_t kB = 128 * kBlk;
@@ -544,7 +550,7 @@ struct SplitSmem {
   static constexpr uint32_t kStaging = kEpiWarps * kStageBytes;
   static constexpr uint32_t kTable = 2 * (kMaxExperts + 1) * 4 + 8;
   static constexpr int kBufs = 3;  // accumulators in flight; a fourth parks one
-  static constexpr uint32_t kBars = (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static constexpr uint32_t kBars = (2 * kStages + 2 * kBufs + 1) * 8 + 16 + 2 * sizeof(SplitTile);
   static constexpr uint32_t kTotal = kRing + kStaging + kTable + kBars + 1024;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(2 * 128 * 128 * 4 <= kRing, "partial sums reuse the ring");
@@ -559,6 +565,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <OutKind KIND>
 __device__ __forceinline__ void put_four(uint8_t *y, int64_t i, const float (&v)[4]) {
@@ -604,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Groups g;
   g.row = reinterpret_cast<int *>(tmem_slot + 4);
   g.tile = g.row + kMaxExperts + 1;
+  SplitTile *split = reinterpret_cast<SplitTile *>(g.tile + kMaxExperts + 1);  // [2]: slots 0 and 1
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntn = (N + 127) / 128, nk = (K + kBlk - 1) / kBlk;
@@ -729,7 +738,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(drain, 0, nullptr, err);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // ---------------- the split tiles, worked out while the weights stream ----------------
+    if (lane == 0) {
+      const int slot = warp - 2;
+      SplitTile m{};
+      if (S > 1 && w1 > w0) {
+        const int lt = (int)(slot == 0 ? w0 / nk : (w1 - 1) / nk);
+        const int64_t i0 = (int64_t)lt * nk, i1 = i0 + nk;
+        if (slot == 0 ? i0 < w0 : (i0 >= w0 && i1 > w1)) {
+          // its contributors: the CTAs with its first to its last item
+          m.ra = (int)(((i0 + 1) * S - 1) / items);
+          m.cnt = (int)((i1 * S - 1) / items) - m.ra + 1;
+          Place p;
+          p.find(g, E, c + lt * C, 128);
+          m.e = p.e;
+          m.row = p.row0 + p.mb * 128;
+          m.rows = min(128, p.rows - p.mb * 128);
+          m.n = p.nb * 128;
+        }
+      }
+      split[slot] = m;
+    }
+    __syncwarp();
+  } else {
     // ---------------- epilogue: a row per lane, 64 columns per warp ----------------
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 64;
@@ -740,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     out.N = N;
     out.lane = lane;
     uint32_t ab = 0, aphase = 0;
-    bool ok = true, parked = false;
+    bool ok = true, parked = false, parked_row = false;
     float2 acc[32];  // fp32 sums; for INT8 the bits of int32 sums
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -764,6 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = out.row0 < out.row_end && n0 < N;  // uniform over the warp
       const int row = min(out.row0 + lane, T - 1);
       w += kend - kb0;
+      // this tile's scales, on their way while its blocks are multiplied
+      const float dx = kBlock ? 0.0f : __ldg(x_scale + row);
+      if (!kBlock && lane < 2 && n0 + lane * 32 < N) prefetch_l2(w_scale + (int64_t)p.e * N + n0 + lane * 32);
       if constexpr (kBlock) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -822,7 +857,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (kb0 == 0 && kend == nk) {  // a whole tile
         if (mine) {
-          const float dx = kBlock ? 0.0f : __ldg(x_scale + row);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[32];
@@ -848,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (w < w1) {  // the end of a tile begun by an earlier CTA, with more to come: parked in TMEM
         parked = true;
+        parked_row = out.row0 + lane < out.row_end;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t r[16];
@@ -865,11 +900,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // partial sums into the ring, which no load or MMA uses any more:
       // [slot][row of the tile][channel], slot 0 for a tile begun by an
       // earlier CTA, slot 1 for one that a later CTA ends; 16-byte chunks
-      // swizzled by row
+      // swizzled by row; only the group's rows
       const int r = quarter * 32 + lane;
       uint4 *mine4 = reinterpret_cast<uint4 *>(smem) + r * 32;
       const bool one = w0 / nk == (w1 - 1) / nk;  // the CTA's items are of one tile
-      if (w1 > w0 && (w1 % nk != 0 || (one && w0 % nk != 0))) {
+      if (w1 > w0 && out.row0 + lane < out.row_end && (w1 % nk != 0 || (one && w0 % nk != 0))) {
         uint4 *d = mine4 + (one && w0 % nk != 0 ? 0 : 128 * 32);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -882,6 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[16];
           tmem_ld16(taddr + kBufs * 128 + q * 16, v);
           tmem_ld_wait();
+          if (parked_row)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mine4[(half * 16 + q * 4 + j) ^ (r & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -893,52 +929,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   if (S > 1) {
     cluster_sync();  // every CTA's partial sums are written
-    if (w1 > w0) {
-      Place p;
 #pragma unroll 1
-      for (int slot = 0; slot < 2; ++slot) {
-        // the split tile, if there is one
-        const int lt = (int)(slot == 0 ? w0 / nk : (w1 - 1) / nk);
-        const int64_t i0 = (int64_t)lt * nk, i1 = i0 + nk;
-        if (slot == 0 ? i0 == w0 : (i0 < w0 || i1 <= w1)) continue;
-        // its contributors: the CTAs with its first to its last item
-        const int ra = (int)(((i0 + 1) * S - 1) / items), rb = (int)((i1 * S - 1) / items), cnt = rb - ra + 1;
-        p.find(g, E, c + lt * C, 128);
-        const int rows = min(128, p.rows - p.mb * 128), row = p.row0 + p.mb * 128;
-        const int u1 = rows * 32 * (rank - ra + 1) / cnt;  // four channels of one row each
-        for (int u = rows * 32 * (rank - ra) / cnt + threadIdx.x; u < u1; u += kThreads) {
-          const int t = u >> 5, n = p.nb * 128 + (u & 31) * 4;
-          const uint32_t at = smem_u32(smem) + (uint32_t)(t * 32 + ((u & 31) ^ (t & 7))) * 16;
-          uint32_t part[kMaxSplit][4];
+    for (int slot = 0; slot < 2; ++slot) {
+      const SplitTile m = split[slot];
+      if (m.cnt == 0) continue;
+      const int u1 = m.rows * 32 * (rank - m.ra + 1) / m.cnt;  // four channels of one row each
+      for (int u = m.rows * 32 * (rank - m.ra) / m.cnt + threadIdx.x; u < u1; u += kThreads) {
+        const int r = u >> 5, row = m.row + r, n = m.n + (u & 31) * 4;
+        const uint32_t at = smem_u32(smem) + (uint32_t)(r * 32 + ((u & 31) ^ (r & 7))) * 16;
+        uint32_t part[kMaxSplit][4];
 #pragma unroll
-          for (int q = 0; q < kMaxSplit; ++q)
-            if (q < cnt) {  // the first contributor began the tile: its slot 1
-              const uint4 v = ld_shared_cluster_v4(mapa_shared(at + (q == 0 ? 128 * 128 * 4 : 0), ra + q));
-              part[q][0] = v.x;
-              part[q][1] = v.y;
-              part[q][2] = v.z;
-              part[q][3] = v.w;
-            }
-          if (n < N) {
-            float v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t sum = part[0][k];
-#pragma unroll
-              for (int q = 1; q < kMaxSplit; ++q)
-                if (q < cnt) {
-                  if constexpr (kF8) {
-                    sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(part[q][k])));
-                  } else {
-                    sum += part[q][k];
-                  }
-                }
-              v[k] = acc_value<kF8>(sum);
-              if constexpr (!kBlock)
-                v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row + t)), __ldg(w_scale + (int64_t)p.e * N + n + k));
-            }
-            put_four<KIND>(y, (int64_t)(row + t) * ldy + n, v);
+        for (int q = 0; q < kMaxSplit; ++q)
+          if (q < m.cnt) {  // the first contributor began the tile: its slot 1
+            const uint4 v = ld_shared_cluster_v4(mapa_shared(at + (q == 0 ? 128 * 128 * 4 : 0), m.ra + q));
+            part[q][0] = v.x;
+            part[q][1] = v.y;
+            part[q][2] = v.z;
+            part[q][3] = v.w;
           }
+        if (n < N) {
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t sum = part[0][k];
+#pragma unroll
+            for (int q = 1; q < kMaxSplit; ++q)
+              if (q < m.cnt) {
+                if constexpr (kF8) {
+                  sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(part[q][k])));
+                } else {
+                  sum += part[q][k];
+                }
+              }
+            v[k] = acc_value<kF8>(sum);
+            if constexpr (!kBlock)
+              v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row)), __ldg(w_scale + (int64_t)m.e * N + n + k));
+          }
+          put_four<KIND>(y, (int64_t)row * ldy + n, v);
         }
       }
     }
