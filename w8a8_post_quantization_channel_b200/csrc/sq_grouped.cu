@@ -996,18 +996,19 @@ struct SplitPlan {
   int64_t cost = INT64_MAX;
 };
 
-// The split with the least cost.  One that splits tiles pays about 14 blocks
-// for its two cluster barriers and the partial sums (4096 x 4096 at 128 rows:
-// 18.0 us unsplit, 14.9, 12.9 and 11.7 us with S = 2, 3 and 4).  Every CTA of a
-// split cluster gets items (nk >= S), so that a tile's contributors are
-// consecutive.
+// The split with the least cost.  One that splits tiles pays about 4 + S / 2
+// blocks for its two cluster barriers and the partial sums (11008 x 4096 at
+// one row: 16.7 us unsplit, 15.3 with S = 3, 15.0 with S = 6; 4096 x 4096 at
+// 128 rows: 16.5 us unsplit, 13.7, 11.8 and 10.8 with S = 2, 3 and 4, 13.8 with
+// S = 8, of which fewer clusters fit).  Every CTA of a split cluster gets items
+// (nk >= S), so that a tile's contributors are consecutive.
 template <GScale SC, OutKind KIND>
 SplitPlan plan_split(int dev, int64_t tiles, int64_t nk) {
   SplitPlan best;
   for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
     const int64_t cap = split_capacity<SC, KIND>(dev, S), C = tiles < cap ? tiles : cap;
     if (C <= 0) continue;
-    const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 14 : 0);
+    const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 4 + S / 2 : 0);
     if (cost < best.cost) {
       best.S = S;
       best.C = (int)C;
