@@ -426,72 +426,51 @@ def sq_w8a8_accumulate_e4m3(xq: torch.Tensor, wq: torch.Tensor, acc=None, worksp
 
 # ---------------------------------------------------------------------------
 # FP8 (E4M3) with one scale per block of 128, and linears over rows grouped
-# by expert.  These calls check every tensor (type, shape, layout, device),
-# run on the tensors' own device whichever is current, and allocate their
-# results on the stream they launch on.
+# by expert.  Their marshalling is native (csrc/sq_binding.cpp): it checks
+# every tensor (type, shape, layout, device), runs on the tensors' own device
+# whichever is current, and allocates results on the stream it launches on.
 # ---------------------------------------------------------------------------
-
-def _blocks(n: int) -> int:
-    """Blocks of 128 that cover n values."""
-    return -(-n // 128)
+_native = None
 
 
-def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> None:
-    """t is a contiguous tensor of this type and shape on `device`."""
-    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype} not supported ({dtype})")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not {t.device}")
-    raise ValueError(f"{name} must be contiguous")
+def _marshal():
+    """The native part of this binding (built in-tree when it is missing or stale)."""
+    global _native
+    if _native is None:
+        lib()
+        from . import build as _build
+        try:
+            _build.build_binding()
+        except Exception as e:  # no compiler: only an existing one will do
+            if not os.path.exists(_build.BINDING):
+                raise RuntimeError(f"_binding.so is missing and cannot be built: {e}") from e
+        from . import _binding as native
+        native.init(_LIB_PATH)
+        _native = native
+    return _native
 
 
-def _elsewhere(device, stream) -> bool:
-    """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != torch._C._cuda_getDevice()
-
-
-def _at(device, stream):
-    """Context in which `device` and the stream to launch on are current."""
-    if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+def _at(t: torch.Tensor, stream):
+    """Context in which the stream to launch on is current (for the allocations too)."""
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return torch.cuda.stream(stream)
 
 
-def _handle(device) -> int:
-    """The current stream's handle (torch's stream object costs more to build than a launch)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _done(r, what: str):
+    """The native call's result; a status that it returned instead raises."""
+    if r.__class__ is int:
+        _check(r, what)
+    return r
 
 
 def sq_quant_act_e4m3_block(x: torch.Tensor, inv_smooth=None, xq=None, x_scale=None, stream=None):
     """(xq [M,K] uint8 E4M3, x_scale [M, ceil(K/128)] = absmax/448 per token and
     128 channels) of x * inv_smooth (None: of x)."""
-    _rowmajor(x, "x")
-    dev = x.device
-    if _elsewhere(dev, stream):
-        with _at(dev, stream):
+    if stream is not None:
+        with _at(x, stream):
             return sq_quant_act_e4m3_block(x, inv_smooth, xq, x_scale)
-    M, K = x.shape
-    dt, KB = _dtype(x, "x"), _blocks(K)
-    if inv_smooth is not None:
-        _expect(inv_smooth, "inv_smooth", torch.float32, (K,), dev)
-    if xq is None:
-        xq = torch.empty(M, K, dtype=torch.uint8, device=dev)
-    else:
-        _expect(xq, "xq", torch.uint8, (M, K), dev)
-    if x_scale is None:
-        x_scale = torch.empty(M, KB, dtype=torch.float32, device=dev)
-    else:
-        _expect(x_scale, "x_scale", torch.float32, (M, KB), dev)
-    _check(lib().sq_quant_act_e4m3_block(x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K,
-                                         None if inv_smooth is None else inv_smooth.data_ptr(), xq.data_ptr(),
-                                         x_scale.data_ptr(), _handle(dev)), "sq_quant_act_e4m3_block")
-    return xq, x_scale
+    return _done(_marshal().quant_act(x, inv_smooth, xq, x_scale), "sq_quant_act_e4m3_block")
 
 
 def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float = 0.5, wq=None, w_scale=None,
@@ -501,98 +480,21 @@ def sq_smooth_quant_weight_e4m3_block(w: torch.Tensor, amax=None, alpha: float =
     feeds, [E, N, K] (they share s); wq has w's shape (uint8), w_scale is
     [(E,) ceil(N/128), ceil(K/128)].  amax None: no smoothing, s and inv_s are
     returned as given (None)."""
-    if w.dim() not in (2, 3) or w.stride(-1) != 1:
-        raise ValueError("w must be a 2-D or 3-D tensor with unit column stride")
-    if not w.is_cuda:
-        raise ValueError("w must be on a CUDA device")
-    dev = w.device
-    if _elsewhere(dev, stream):
-        with _at(dev, stream):
+    if stream is not None:
+        with _at(w, stream):
             return sq_smooth_quant_weight_e4m3_block(w, amax, alpha, wq, w_scale, smooth, inv_smooth)
-    E, (N, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
-    ldw = w.stride(-2) if N > 1 else (w.stride(0) if w.dim() == 3 and E > 1 else K)
-    if w.dim() == 3 and E > 1 and w.stride(0) != N * ldw:
-        raise ValueError("w's experts must follow one another (stride(0) == N * stride(1))")
-    dt = _dtype(w, "w")
-    scale_shape = (*w.shape[:-2], _blocks(N), _blocks(K))
-    for t, name in ((amax, "amax"), (smooth, "smooth"), (inv_smooth, "inv_smooth")):
-        if t is not None:
-            _expect(t, name, torch.float32, (K,), dev)
-    if wq is None:
-        wq = torch.empty(*w.shape, dtype=torch.uint8, device=dev)
-    else:
-        _expect(wq, "wq", torch.uint8, w.shape, dev)
-    if w_scale is None:
-        w_scale = torch.empty(*scale_shape, dtype=torch.float32, device=dev)
-    else:
-        _expect(w_scale, "w_scale", torch.float32, scale_shape, dev)
-    if amax is not None:
-        smooth = torch.empty_like(amax) if smooth is None else smooth
-        inv_smooth = torch.empty_like(amax) if inv_smooth is None else inv_smooth
-    _check(lib().sq_smooth_quant_weight_e4m3_block(
-        w.data_ptr(), dt, E, N, K, ldw, None if amax is None else amax.data_ptr(), alpha, wq.data_ptr(),
-        w_scale.data_ptr(), None if smooth is None else smooth.data_ptr(),
-        None if inv_smooth is None else inv_smooth.data_ptr(), _handle(dev)), "sq_smooth_quant_weight_e4m3_block")
-    return wq, w_scale, smooth, inv_smooth
-
-
-def _out_matrix(x: torch.Tensor, y, T: int, N: int, out_dtype) -> torch.Tensor:
-    """y checked, or a new [T, N] matrix of out_dtype beside x."""
-    if y is None:
-        if out_dtype not in _DT:
-            raise ValueError(f"out_dtype {out_dtype} not supported (float32/float16/bfloat16)")
-        return torch.empty(T, N, dtype=out_dtype, device=x.device)
-    _rowmajor(y, "y")
-    _dtype(y, "y")
-    if y.shape != (T, N):
-        raise ValueError(f"y must have shape {(T, N)}, not {tuple(y.shape)}")
-    if y.device != x.device:
-        raise ValueError(f"y must be on {x.device}, not {y.device}")
-    return y
+    return _done(_marshal().quant_weight(w, amax, alpha, wq, w_scale, smooth, inv_smooth),
+                 "sq_smooth_quant_weight_e4m3_block")
 
 
 def sq_w8a8_linear_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
                               out_dtype=torch.bfloat16, y=None, stream=None) -> torch.Tensor:
     """y [M,N] = dequantized xq times dequantized wq^T for block-scaled E4M3
     codes: x_scale [M, ceil(K/128)], w_scale [ceil(N/128), ceil(K/128)]."""
-    _rowmajor(xq, "xq")
-    dev = xq.device
-    if _elsewhere(dev, stream):
-        with _at(dev, stream):
+    if stream is not None:
+        with _at(xq, stream):
             return sq_w8a8_linear_e4m3_block(xq, x_scale, wq, w_scale, out_dtype, y)
-    M, K = xq.shape
-    N, KB = wq.shape[0], _blocks(K)
-    _expect(xq, "xq", torch.uint8, (M, K), dev)
-    _expect(wq, "wq", torch.uint8, (N, K), dev)
-    _expect(x_scale, "x_scale", torch.float32, (M, KB), dev)
-    _expect(w_scale, "w_scale", torch.float32, (_blocks(N), KB), dev)
-    y = _out_matrix(xq, y, M, N, out_dtype)
-    _check(lib().sq_w8a8_linear_e4m3_block(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-                                           M, N, K, y.data_ptr(), _DT[y.dtype], y.stride(0) if M > 1 else N,
-                                           _handle(dev)), "sq_w8a8_linear_e4m3_block")
-    return y
-
-
-def _grouped(name: str, code_dtype, block: bool, xq, x_scale, wq, w_scale, offsets, out_dtype, y, stream):
-    _rowmajor(xq, "xq")
-    dev = xq.device
-    if _elsewhere(dev, stream):
-        with _at(dev, stream):
-            return _grouped(name, code_dtype, block, xq, x_scale, wq, w_scale, offsets, out_dtype, y, None)
-    if wq.dim() != 3:
-        raise ValueError("wq must be a 3-D tensor [E, N, K]")
-    T, K = xq.shape
-    E, N, _ = wq.shape
-    _expect(xq, "xq", code_dtype, (T, K), dev)
-    _expect(wq, "wq", code_dtype, (E, N, K), dev)
-    _expect(x_scale, "x_scale", torch.float32, (T, _blocks(K)) if block else (T,), dev)
-    _expect(w_scale, "w_scale", torch.float32, (E, _blocks(N), _blocks(K)) if block else (E, N), dev)
-    _expect(offsets, "offsets", torch.int32, (E + 1,), dev)
-    y = _out_matrix(xq, y, T, N, out_dtype)
-    _check(getattr(lib(), name)(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
-                                offsets.data_ptr(), T, E, N, K, y.data_ptr(), _DT[y.dtype],
-                                y.stride(0) if T > 1 else N, _handle(dev)), name)
-    return y
+    return _done(_marshal().linear(0, xq, x_scale, wq, w_scale, None, out_dtype, y), "sq_w8a8_linear_e4m3_block")
 
 
 def sq_w8a8_linear_grouped(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
@@ -602,16 +504,20 @@ def sq_w8a8_linear_grouped(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Te
     offsets [E+1] is int32 on the device, non-decreasing, and is not read on
     the host.  Rows in no group keep what y held (an allocated y:
     unspecified values)."""
-    return _grouped("sq_w8a8_linear_grouped", torch.int8, False, xq, x_scale, wq, w_scale, offsets, out_dtype, y,
-                    stream)
+    if stream is not None:
+        with _at(xq, stream):
+            return sq_w8a8_linear_grouped(xq, x_scale, wq, w_scale, offsets, out_dtype, y)
+    return _done(_marshal().linear(1, xq, x_scale, wq, w_scale, offsets, out_dtype, y), "sq_w8a8_linear_grouped")
 
 
 def sq_w8a8_linear_grouped_e4m3(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
                                 offsets: torch.Tensor, out_dtype=torch.bfloat16, y=None,
                                 stream=None) -> torch.Tensor:
     """sq_w8a8_linear_grouped for E4M3 codes (uint8)."""
-    return _grouped("sq_w8a8_linear_grouped_e4m3", torch.uint8, False, xq, x_scale, wq, w_scale, offsets, out_dtype,
-                    y, stream)
+    if stream is not None:
+        with _at(xq, stream):
+            return sq_w8a8_linear_grouped_e4m3(xq, x_scale, wq, w_scale, offsets, out_dtype, y)
+    return _done(_marshal().linear(2, xq, x_scale, wq, w_scale, offsets, out_dtype, y), "sq_w8a8_linear_grouped_e4m3")
 
 
 def sq_w8a8_linear_grouped_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
@@ -619,8 +525,11 @@ def sq_w8a8_linear_grouped_e4m3_block(xq: torch.Tensor, x_scale: torch.Tensor, w
                                       y=None, stream=None) -> torch.Tensor:
     """sq_w8a8_linear_grouped for block-scaled E4M3 codes (uint8): x_scale
     [T, ceil(K/128)], w_scale [E, ceil(N/128), ceil(K/128)]."""
-    return _grouped("sq_w8a8_linear_grouped_e4m3_block", torch.uint8, True, xq, x_scale, wq, w_scale, offsets,
-                    out_dtype, y, stream)
+    if stream is not None:
+        with _at(xq, stream):
+            return sq_w8a8_linear_grouped_e4m3_block(xq, x_scale, wq, w_scale, offsets, out_dtype, y)
+    return _done(_marshal().linear(3, xq, x_scale, wq, w_scale, offsets, out_dtype, y),
+                 "sq_w8a8_linear_grouped_e4m3_block")
 
 
 # Size of the scratch array compiled into libsq.so for the allocation-free

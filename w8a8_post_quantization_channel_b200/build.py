@@ -1,4 +1,5 @@
-"""Builds libsq.so in-tree from csrc/*.cu with nvcc for sm_100a.
+"""Builds libsq.so in-tree from csrc/*.cu with nvcc for sm_100a, and the
+binding's native part, _binding.so, from csrc/sq_binding.cpp.
 
 Usage: python -m w8a8_post_quantization_channel_b200.build [--force]
 """
@@ -17,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsq.so")
+BINDING_SRC = os.path.join(CSRC, "sq_binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # No fast-math: IEEE division/sqrt and no FMA contraction keep every
@@ -34,7 +37,8 @@ def nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    files = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    files = glob.glob(os.path.join(CSRC, "*.cu*")) + glob.glob(os.path.join(CSRC, "*.h"))
+    files += glob.glob(os.path.join(INCLUDE, "*.h"))
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -47,6 +51,28 @@ def _compile(src: str, extra: list[str]) -> str:
     if r.stderr.strip():
         sys.stderr.write(r.stderr)
     return obj
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so against the torch that runs this."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "sq.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -69,3 +95,4 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose_ptxas="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
