@@ -26,6 +26,22 @@ constexpr int kThreads = 384;      // TMA, MMA and two idle warps, then eight ep
 constexpr int kEpiWarps = 8;
 constexpr int kStageBytes = 4096;  // an epilogue warp's output staging: 32 rows x 128 bytes
 
+// Whether a barrier's phase has completed, without waiting.  The thread that
+// issues the MMAs asks for the next step's barriers before it issues this
+// step's MMAs, which hides the answers' latency behind them: one thread's
+// waits and commits, not the operands' loads, bounded both kernels here.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Arrive on an mbarrier of another CTA of the cluster (shared::cluster
 // address).  Without .release.cluster, which waits for the thread's earlier
 // global stores: the TMEM reads that it publishes are ordered by
@@ -211,7 +227,7 @@ __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.
 
 // Persistent over 256 x 256 tiles of Y: a pair of CTAs works on one tile
 // (tcgen05 cta_group::2), each with 128 rows of Xq and half of the tile's rows
-// of Wq in its shared memory; the leader's MMA thread drives both.  Warp 0 loads, warp 1 issues the MMAs, warps 4-11 (two per
+// of Wq in its shared memory; the leader's MMA thread drives both.  Warps 0 and 2 load, warp 1 issues the MMAs, warps 4-11 (two per
 // TMEM lane quarter, each half of the columns) dequantize and store.
 template <GScale SC, OutKind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // the loaders of A and of B
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -273,28 +289,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = g.tile[E];
 
   if (warp < 4) regs_give();
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
-      // ---------------- TMA producer ----------------
+      // ---------------- TMA producers: warp 0 the rows of Xq, warp 2 those of Wq ----------------
+      const bool x = warp == 0;
+      const CUtensorMap *tm = x ? &tmA : &tmB;
+      uint8_t *const ring = x ? sA : sB;
+      const uint32_t bytes = x ? L::kA : L::kB;
       uint32_t stage = 0, phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
       Place p;
       for (int tile = unit; tile < tiles && ok; tile += units) {
         p.find(g, E, tile, kPairRows);
-        const int row_a = p.row0 + p.mb * kPairRows + rank * 128, row_b = p.e * N + p.nb * kPairCols + rank * (kPairCols / 2);
+        const int row = x ? p.row0 + p.mb * kPairRows + rank * 128 : p.e * N + p.nb * kPairCols + rank * (kPairCols / 2);
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, err)) {
             ok = false;
             break;
           }
           if (leader) {  // its barrier counts both CTAs' copies
-            mbar_arrive_expect_tx(&full[stage], 2 * (L::kA + L::kB));
+            mbar_arrive_expect_tx(&full[stage], 2 * bytes);
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
-          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-          tma_load_2d_pair(&tmA, bar, sA + stage * L::kA, kb * kBlk, row_a);
-          tma_load_2d_pair(&tmB, bar, sB + stage * L::kB, kb * kBlk, row_b);
+          tma_load_2d_pair(tm, mapa_shared(smem_u32(&full[stage]), 0), ring + stage * bytes, kb * kBlk, row);
           if (++stage == L::kStages) {
             stage = 0;
             phase ^= 1;
@@ -306,40 +324,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (armed & (1u << s)) mbar_wait(&full[s], (armed_parity >> s) & 1u, nullptr, err);
       }
     }
-    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc8<kF8>(kPairRows, kPairCols);
       uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
-      bool ok = true;
+      bool ok = true, full_seen = false, tempty_seen = false;
       for (int tile = unit; tile < tiles && ok; tile += units) {
         for (int kb = 0; kb < nk; ++kb) {
           const bool first = kBlock || kb == 0, last = kBlock || kb == nk - 1;
-          if (first && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) {
+          if (first && !tempty_seen && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) {
             ok = false;
             break;
           }
-          if (!mbar_wait(&full[stage], phase, abort_flag, err)) {
+          if (!full_seen && !mbar_wait(&full[stage], phase, abort_flag, err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + stage * L::kA));
-          const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + stage * L::kB));
-#pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k)
-            umma8_pair<kF8>(tmem_base + ab * kPairCols, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
-          umma_commit_both(&empty[stage]);
-          if (last) {
-            if (!kBlock) umma_commit_both(&tfull[ab]);
-            ab ^= 1;
-            if (ab == 0) aphase ^= 1;
-          }
+          const uint32_t at = stage, d = tmem_base + ab * kPairCols;
           if (++stage == L::kStages) {
             stage = 0;
             phase ^= 1;
           }
+          if (last) {
+            ab ^= 1;
+            if (ab == 0) aphase ^= 1;
+          }
+          full_seen = mbar_test(&full[stage], phase);
+          if (last) tempty_seen = mbar_test(&tempty[ab], aphase ^ 1);
+          const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + at * L::kA));
+          const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + at * L::kB));
+#pragma unroll
+          for (int k = 0; k < kBlk / 32; ++k)
+            umma8_pair<kF8>(d, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
+          umma_commit_both(&empty[at]);
+          if (!kBlock && last) umma_commit_both(&tfull[ab ^ 1]);
         }
       }
       // every MMA issued above must finish before TMEM is released
@@ -619,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // the loaders of A and of B
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < kBufs; ++b) {
@@ -651,9 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t items = (int64_t)max(0, (g.tile[E] - c + C - 1) / C) * nk;
   const int64_t w0 = items * rank / S, w1 = items * (rank + 1) / S;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
-      // ---------------- TMA producer ----------------
+      // ---------------- TMA producers: warp 0 the rows of Xq, warp 2 those of Wq ----------------
+      const bool x = warp == 0;
       const uint64_t policy = policy_evict_first();
       uint32_t stage = 0, phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
@@ -675,17 +696,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], L::kB + boxes * 32 * kBlk);
-          if (once) {
-            tma_load_2d_hint(&tmB, &full[stage], sB + stage * L::kB, kb * kBlk, row_b, policy);
-          } else {
-            tma_load_2d(&tmB, &full[stage], sB + stage * L::kB, kb * kBlk, row_b);
-          }
-          if (boxes == 4) {
-            tma_load_2d(&tmA, &full[stage], sA + stage * L::kA, kb * kBlk, row_a);
+          uint8_t *const dst = x ? sA + stage * L::kA : sB + stage * L::kB;
+          mbar_arrive_expect_tx(&full[stage], x ? boxes * 32 * kBlk : L::kB);
+          if (!x) {
+            if (once) {
+              tma_load_2d_hint(&tmB, &full[stage], dst, kb * kBlk, row_b, policy);
+            } else {
+              tma_load_2d(&tmB, &full[stage], dst, kb * kBlk, row_b);
+            }
+          } else if (boxes == 4) {
+            tma_load_2d(&tmA, &full[stage], dst, kb * kBlk, row_a);
           } else {
             for (int i = 0; i < boxes; ++i)
-              tma_load_2d(&tmA32, &full[stage], sA + stage * L::kA + i * 32 * kBlk, kb * kBlk, row_a + i * 32);
+              tma_load_2d(&tmA32, &full[stage], dst + i * 32 * kBlk, kb * kBlk, row_a + i * 32);
           }
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -706,42 +729,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc8<kF8>(128, 128);
       uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
-      bool ok = true;
-      int64_t seg = w0 + nk - w0 % nk;  // the tile's last item + 1
-      for (int64_t w = w0; w < w1; ++w) {
-        const bool first = kBlock || w == w0 || w == seg;
-        if (w == seg) seg += nk;
-        const bool last = kBlock || w + 1 == seg || w + 1 == w1;
-        if (first && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) break;
-        if (!mbar_wait(&full[stage], phase, abort_flag, err)) break;
+      bool full_seen = false, tempty_seen = false, first = true;
+      int left = nk - (int)(w0 % nk);  // blocks to the end of the tile
+      for (int64_t n = w1 - w0; n > 0; --n) {
+        const bool last = kBlock || left == 1 || n == 1;
+        if (first && !tempty_seen && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) break;
+        if (!full_seen && !mbar_wait(&full[stage], phase, abort_flag, err)) break;
         tc_fence_after();
-        const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + stage * L::kA));
-        const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + stage * L::kB));
-#pragma unroll
-        for (int k = 0; k < kBlk / 32; ++k)
-          umma8<kF8>(tmem_base + ab * 128, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
-        umma_commit(&empty[stage]);
-        if (last) {
-          umma_commit(&tfull[ab]);
-          if (++ab == kBufs) {
-            ab = 0;
-            aphase ^= 1;
-          }
-        }
+        const uint32_t at = stage, buf = ab, add = first ? 0u : 1u;
         if (++stage == L::kStages) {
           stage = 0;
           phase ^= 1;
         }
+        if (last && ++ab == kBufs) {
+          ab = 0;
+          aphase ^= 1;
+        }
+        full_seen = mbar_test(&full[stage], phase);
+        if (last) tempty_seen = mbar_test(&tempty[ab], aphase ^ 1);
+        const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + at * L::kA));
+        const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + at * L::kB));
+#pragma unroll
+        for (int k = 0; k < kBlk / 32; ++k)
+          umma8<kF8>(tmem_base + buf * 128, a0 + 2 * k, b0 + 2 * k, idesc, k != 0 ? 1u : add);
+        umma_commit(&empty[at]);
+        if (!kBlock && last) umma_commit(&tfull[buf]);
+        first = last;
+        if (--left == 0) left = nk;
       }
       // every MMA issued above must finish before TMEM is released
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, err);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 3) {
     // ---------------- the split tiles, worked out while the weights stream ----------------
-    if (lane == 0) {
-      const int slot = warp - 2;
+    if (lane < 2) {
+      const int slot = lane;
       SplitTile m{};
       if (S > 1 && w1 > w0) {
         const int lt = (int)(slot == 0 ? w0 / nk : (w1 - 1) / nk);
@@ -771,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     out.ldy = ldy;
     out.N = N;
     out.lane = lane;
-    uint32_t ab = 0, aphase = 0;
+    uint32_t ab = 0, aphase = 0, stage = 0, phase = 0;
     bool ok = true, parked = false, parked_row = false;
     float2 acc[32];  // fp32 sums; for INT8 the bits of int32 sums
 #pragma unroll
@@ -808,8 +832,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = kb0; kb < kend; ++kb) {
           const int kn = min(kb + 1, nk - 1);
           const float xn = __ldg(xs + kn), wn = __ldg(ws + kn);  // the next block's scales
-          ok = __all_sync(0xffffffffu, mbar_wait(&tfull[ab], aphase, abort_flag, err));
+          // a block's product is complete when its operands are free again
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, abort_flag, err));
           if (!ok) break;
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
           tc_fence_after();
           const float2 s2 = make_float2(s, s);
           const uint32_t src = taddr + ab * 128;
