@@ -26,20 +26,61 @@ constexpr int kThreads = 384;      // TMA, MMA and two idle warps, then eight ep
 constexpr int kEpiWarps = 8;
 constexpr int kStageBytes = 4096;  // an epilogue warp's output staging: 32 rows x 128 bytes
 
-// Whether a barrier's phase has completed, without waiting.  The thread that
-// issues the MMAs asks for the next step's barriers before it issues this
-// step's MMAs, which hides the answers' latency behind them: one thread's
-// waits and commits, not the operands' loads, bounded both kernels here.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// One 128-channel block's MMAs (four of K = 32), the commit on `done` (of both
+// CTAs for a pair), and whether the barriers of the next step, `full` and
+// `tempty`, have completed their phases: asked for before the MMAs are issued
+// and looked at after the commit, behind the MMAs.  The whole warp runs this
+// and an elected lane issues: descriptors are then warp-uniform values, which
+// the MMAs take from uniform registers (one lane alone: about 290 cycles to
+// issue a block, so 103).
+struct Seen {
+  uint32_t full, tempty;
+};
+#define SQ_MMA4(GROUP, KIND, COMMIT)                                                              \
+  "{\n\t.reg .pred one, first, add, pf, pt;\n\t.reg .b64 a, b;\n\t"                               \
+  "elect.sync _|one, 0xffffffff;\n\t"                                                            \
+  "setp.ne.b32 first, %6, 0;\n\tsetp.eq.b32 add, 0, 0;\n\t"                                      \
+  "mbarrier.test_wait.parity.shared::cta.b64 pf, [%8], %9;\n\t"                                  \
+  "mbarrier.test_wait.parity.shared::cta.b64 pt, [%10], %11;\n\t"                                \
+  "@one tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%2], %3, %4, %5, first;\n\t"            \
+  "add.s64 a, %3, 2;\n\tadd.s64 b, %4, 2;\n\t"                                                  \
+  "@one tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%2], a, b, %5, add;\n\t"                \
+  "add.s64 a, %3, 4;\n\tadd.s64 b, %4, 4;\n\t"                                                  \
+  "@one tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%2], a, b, %5, add;\n\t"                \
+  "add.s64 a, %3, 6;\n\tadd.s64 b, %4, 6;\n\t"                                                  \
+  "@one tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%2], a, b, %5, add;\n\t" COMMIT         \
+  "selp.u32 %0, 1, 0, pf;\n\tselp.u32 %1, 1, 0, pt;\n\t}\n"
+#define SQ_COMMIT1 "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t"
+// one instruction for both CTAs
+#define SQ_COMMIT2                                                                                     \
+  ".reg .b16 both;\n\tmov.b16 both, 3;\n\t"                                                            \
+  "@one tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], both;\n\t"
+#define SQ_MMA4_ARGS                                                                                          \
+  : "=r"(seen.full), "=r"(seen.tempty)                                                                        \
+  : "r"(d), "l"(a0), "l"(b0), "r"(idesc), "r"(add), "r"(smem_u32(done)), "r"(smem_u32(full)), "r"(full_parity), \
+    "r"(smem_u32(tempty)), "r"(tempty_parity)                                                                 \
+  : "memory"
+template <int CG, bool F8>
+__device__ __forceinline__ Seen mma_block(uint32_t d, uint64_t a0, uint64_t b0, uint32_t idesc, uint32_t add,
+                                          uint64_t *done, uint64_t *full, uint32_t full_parity, uint64_t *tempty,
+                                          uint32_t tempty_parity) {
+  Seen seen;
+  if constexpr (CG == 1 && F8) {
+    asm volatile(SQ_MMA4("1", "f8f6f4", SQ_COMMIT1) SQ_MMA4_ARGS);
+  } else if constexpr (CG == 1) {
+    asm volatile(SQ_MMA4("1", "i8", SQ_COMMIT1) SQ_MMA4_ARGS);
+  } else if constexpr (F8) {
+    asm volatile(SQ_MMA4("2", "f8f6f4", SQ_COMMIT2) SQ_MMA4_ARGS);
+  } else {
+    asm volatile(SQ_MMA4("2", "i8", SQ_COMMIT2) SQ_MMA4_ARGS);
+  }
+  return seen;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 
 // Arrive on an mbarrier of another CTA of the cluster (shared::cluster
@@ -52,15 +93,64 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
 }
 
 // Arrive once on the mbarrier at this address in both CTAs of the pair when
-// the MMAs issued so far have completed.  One instruction for both: a commit
-// holds the issuing thread for some 130 cycles, a quarter of a 128-channel
-// block's MMAs.
+// the MMAs issued so far have completed.
 __device__ __forceinline__ void umma_commit_both(uint64_t *bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+
+// The MMA warp's loop, for both kernels: n blocks of 128 channels, `left` of
+// them to the end of the first tile and nk in every later one.  One warp's
+// waits, issues and commits bound it, so the ring's stages are unrolled and a
+// block whose operands are there costs one vote besides its MMAs (with the
+// elected issue, 4096 x 11008 x 4096: INT8 128 -> 115 us, E4M3 144 -> 128,
+// block scales 195 -> 176).  kBlock: every block has an accumulator of its
+// own; otherwise a tile has one, handed over on tfull (with block scales on
+// the stage's own barrier).  Ends early when a wait runs out.
+template <int CG, bool F8, bool kBlock, int kStages, int kBufs, uint32_t kA, uint32_t kB, int kCols>
+__device__ __forceinline__ void mma_loop(uint32_t sA, uint32_t sB, uint64_t *full, uint64_t *empty, uint64_t *tfull,
+                                         uint64_t *tempty, uint32_t tmem, uint32_t idesc, int64_t n, int nk, int left,
+                                         volatile int *abort, unsigned *err) {
+  const uint64_t a0 = desc_sw128_kmajor(sA), b0 = desc_sw128_kmajor(sB);
+  uint32_t phase = 0, buf = 0, bphase = 1;
+  bool first = true;
+  Seen seen = {0u, 0u};
+#pragma unroll 1
+  for (;; phase ^= 1) {
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) {
+      if (n == 0) return;
+      --n;
+      const bool last = kBlock || left == 1 || n == 0;
+      if (!__all_sync(0xffffffffu, seen.full && (!first || seen.tempty))) {
+        if (!__all_sync(0xffffffffu, (!first || mbar_wait(&tempty[buf], bphase, abort, err)) &&
+                                         mbar_wait(&full[st], phase, abort, err)))
+          return;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + buf * kCols, add = kBlock || first ? 0u : 1u;
+      uint64_t *const done = tfull + buf;
+      if (last && ++buf == kBufs) {
+        buf = 0;
+        bphase ^= 1;
+      }
+      const int next = (st + 1) % kStages;
+      seen = mma_block<CG, F8>(d, a0 + st * (kA >> 4), b0 + st * (kB >> 4), idesc, add, &empty[st], &full[next],
+                               phase ^ (next == 0 ? 1u : 0u), &tempty[buf], bphase);
+      if (!kBlock && last && elect_one()) {
+        if constexpr (CG == 2) {
+          umma_commit_both(done);
+        } else {
+          umma_commit(done);
+        }
+      }
+      first = last;
+      if (!kBlock && --left == 0) left = nk;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -253,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   g.row = reinterpret_cast<int *>(tmem_slot + 4);
   g.tile = g.row + kMaxExperts + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const bool leader = rank == 0;
   const int unit = blockIdx.x / 2, units = gridDim.x / 2;
@@ -282,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();  // prologue done; the previous kernel's results are visible from here on
   pdl_trigger();
   build_groups(g, offsets, E, T, kPairRows, ntn);
@@ -325,46 +415,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc8<kF8>(kPairRows, kPairCols);
-      uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
-      bool ok = true, full_seen = false, tempty_seen = false;
-      for (int tile = unit; tile < tiles && ok; tile += units) {
-        for (int kb = 0; kb < nk; ++kb) {
-          const bool first = kBlock || kb == 0, last = kBlock || kb == nk - 1;
-          if (first && !tempty_seen && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          if (!full_seen && !mbar_wait(&full[stage], phase, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = stage, d = tmem_base + ab * kPairCols;
-          if (++stage == L::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (last) {
-            ab ^= 1;
-            if (ab == 0) aphase ^= 1;
-          }
-          full_seen = mbar_test(&full[stage], phase);
-          if (last) tempty_seen = mbar_test(&tempty[ab], aphase ^ 1);
-          const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + at * L::kA));
-          const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + at * L::kB));
-#pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k)
-            umma8_pair<kF8>(d, a0 + 2 * k, b0 + 2 * k, idesc, (k != 0 || !first) ? 1u : 0u);
-          umma_commit_both(&empty[at]);
-          if (!kBlock && last) umma_commit_both(&tfull[ab ^ 1]);
-        }
-      }
+      const int64_t mine = tiles > unit ? (tiles - unit + units - 1) / units : 0;  // this pair's tiles
+      mma_loop<2, kF8, kBlock, L::kStages, 2, L::kA, L::kB, kPairCols>(
+          smem_u32(sA), smem_u32(sB), full, empty, tfull, tempty, tmem_base, idesc8<kF8>(kPairRows, kPairCols),
+          mine * nk, nk, nk, abort_flag, err);
       // every MMA issued above must finish before TMEM is released
-      umma_commit_pair(mapa_shared(smem_u32(drain), 0));
-      mbar_wait(drain, 0, nullptr, err);
+      if (elect_one()) {
+        umma_commit_pair(mapa_shared(smem_u32(drain), 0));
+        mbar_wait(drain, 0, nullptr, err);
+      }
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -550,9 +611,11 @@ cudaError_t run_pair(const GroupedArgs &a, int cap, cudaStream_t st) {
 // block) items evenly, so a CTA holds the end of one tile, whole tiles, and
 // the beginning of another.  Split tiles' partial sums meet in shared memory:
 // every contributor adds up its share of the tile over all of them, in rank
-// order, so results do not depend on timing.  No workspace, no atomics.  Rows
-// of Xq are loaded 32 at a time, as many as the group has: the MMA's other
-// rows hold what the ring held before, and go nowhere.
+// order, so results do not depend on timing.  No workspace, no atomics.  Of
+// Xq's rows a box of 32, 64 or 128 is loaded, whichever holds what the group
+// has: the MMA's other rows hold what the ring held before, and go nowhere.
+// (One box a block: up to four of 32 rows cost the loader 730 cycles a block
+// where one of 128 costs 545, 333 x 4096 x 11008: 34.9 -> 29.4 us.)
 // ---------------------------------------------------------------------------
 constexpr int kMaxSplit = 8;  // CTAs per cluster
 
@@ -586,6 +649,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <OutKind KIND>
@@ -610,10 +677,10 @@ __device__ __forceinline__ void put_four(uint8_t *y, int64_t i, const float (&v)
 
 template <GScale SC, OutKind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
-                         const __grid_constant__ CUtensorMap tmB, const float *__restrict__ x_scale,
-                         const float *__restrict__ w_scale, const int32_t *__restrict__ offsets,
-                         uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N, int K, int S, unsigned *err) {
+    grouped_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
+                         const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmB, const float *__restrict__ x_scale, const float *__restrict__ w_scale,
+                         const int32_t *__restrict__ offsets, uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N,
+                         int K, int S, unsigned *err) {
   using L = SplitSmem;
   constexpr bool kF8 = SC != GScale::I8, kBlock = SC == GScale::Block;
   constexpr int kBufs = L::kBufs;
@@ -634,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   g.tile = g.row + kMaxExperts + 1;
   SplitTile *split = reinterpret_cast<SplitTile *>(g.tile + kMaxExperts + 1);  // [2]: slots 0 and 1
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int ntn = (N + 127) / 128, nk = (K + kBlk - 1) / kBlk;
 
   if (threadIdx.x == 0) {
@@ -650,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmA);
+    prefetch_tmap(&tmA64);
     prefetch_tmap(&tmA32);
     prefetch_tmap(&tmB);
   }
@@ -660,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();  // prologue done; the previous kernel's results are visible from here on
   pdl_trigger();
   build_groups(g, offsets, E, T, 128, ntn);
@@ -685,11 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kend = (int)min((int64_t)nk, w1 - (int64_t)lt * nk);
         p.find(g, E, c + lt * C, 128);
         const int row_a = p.row0 + p.mb * 128, row_b = p.e * N + p.nb * 128;
-        const int boxes = min(4, (p.rows - p.mb * 128 + 31) / 32);  // 32 rows each
+        // as many of the tile's rows as its group has: one box of 32, 64 or 128
+        const int rows = p.rows - p.mb * 128, box = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+        const CUtensorMap *const tm = !x ? &tmB : box == 32 ? &tmA32 : box == 64 ? &tmA64 : &tmA;
+        const uint32_t bytes = x ? box * kBlk : L::kB;
+        const int row = x ? row_a : row_b;
         // an expert's weights that one tile of rows reads once leave L2 first
         // (INT8, 192 rows of 64 experts 2048 -> 1408: 38.2 -> 36.9 us; of no
         // use to a dense weight)
-        const bool once = offsets != nullptr && p.rows <= 128;
+        const bool once = !x && offsets != nullptr && p.rows <= 128;
         w += kend - kb;
         for (; kb < kend; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, err)) {
@@ -697,18 +769,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t *const dst = x ? sA + stage * L::kA : sB + stage * L::kB;
-          mbar_arrive_expect_tx(&full[stage], x ? boxes * 32 * kBlk : L::kB);
-          if (!x) {
-            if (once) {
-              tma_load_2d_hint(&tmB, &full[stage], dst, kb * kBlk, row_b, policy);
-            } else {
-              tma_load_2d(&tmB, &full[stage], dst, kb * kBlk, row_b);
-            }
-          } else if (boxes == 4) {
-            tma_load_2d(&tmA, &full[stage], dst, kb * kBlk, row_a);
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          if (once) {
+            tma_load_2d_hint(tm, &full[stage], dst, kb * kBlk, row, policy);
           } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(&tmA32, &full[stage], dst + i * 32 * kBlk, kb * kBlk, row_a + i * 32);
+            tma_load_2d(tm, &full[stage], dst, kb * kBlk, row);
           }
           armed |= 1u << stage;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -725,39 +790,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc8<kF8>(128, 128);
-      uint32_t stage = 0, phase = 0, ab = 0, aphase = 0;
-      bool full_seen = false, tempty_seen = false, first = true;
-      int left = nk - (int)(w0 % nk);  // blocks to the end of the tile
-      for (int64_t n = w1 - w0; n > 0; --n) {
-        const bool last = kBlock || left == 1 || n == 1;
-        if (first && !tempty_seen && !mbar_wait(&tempty[ab], aphase ^ 1, abort_flag, err)) break;
-        if (!full_seen && !mbar_wait(&full[stage], phase, abort_flag, err)) break;
-        tc_fence_after();
-        const uint32_t at = stage, buf = ab, add = first ? 0u : 1u;
-        if (++stage == L::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-        if (last && ++ab == kBufs) {
-          ab = 0;
-          aphase ^= 1;
-        }
-        full_seen = mbar_test(&full[stage], phase);
-        if (last) tempty_seen = mbar_test(&tempty[ab], aphase ^ 1);
-        const uint64_t a0 = desc_sw128_kmajor(smem_u32(sA + at * L::kA));
-        const uint64_t b0 = desc_sw128_kmajor(smem_u32(sB + at * L::kB));
-#pragma unroll
-        for (int k = 0; k < kBlk / 32; ++k)
-          umma8<kF8>(tmem_base + buf * 128, a0 + 2 * k, b0 + 2 * k, idesc, k != 0 ? 1u : add);
-        umma_commit(&empty[at]);
-        if (!kBlock && last) umma_commit(&tfull[buf]);
-        first = last;
-        if (--left == 0) left = nk;
-      }
-      // every MMA issued above must finish before TMEM is released
+    // ---------------- MMA issuer ----------------
+    mma_loop<1, kF8, kBlock, L::kStages, kBufs, L::kA, L::kB, 128>(
+        smem_u32(sA), smem_u32(sB), full, empty, tfull, tempty, tmem_base, idesc8<kF8>(128, 128), w1 - w0, nk,
+        nk - (int)(w0 % nk), abort_flag, err);
+    // every MMA issued above must finish before TMEM is released
+    if (elect_one()) {
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, err);
     }
@@ -966,6 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = m.rows * 32 * (rank - m.ra) / m.cnt + threadIdx.x; u < u1; u += kThreads) {
         const int r = u >> 5, row = m.row + r, n = m.n + (u & 31) * 4;
         const uint32_t at = smem_u32(smem) + (uint32_t)(r * 32 + ((u & 31) ^ (r & 7))) * 16;
+        if (n >= N) continue;
         uint32_t part[kMaxSplit][4];
 #pragma unroll
         for (int q = 0; q < kMaxSplit; ++q)
@@ -976,30 +1015,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             part[q][2] = v.z;
             part[q][3] = v.w;
           }
-        if (n < N) {
-          float v[4];
+        float v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t sum = part[0][k];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t sum = part[0][k];
 #pragma unroll
-            for (int q = 1; q < kMaxSplit; ++q)
-              if (q < m.cnt) {
-                if constexpr (kF8) {
-                  sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(part[q][k])));
-                } else {
-                  sum += part[q][k];
-                }
+          for (int q = 1; q < kMaxSplit; ++q)
+            if (q < m.cnt) {
+              if constexpr (kF8) {
+                sum = __float_as_uint(__fadd_rn(__uint_as_float(sum), __uint_as_float(part[q][k])));
+              } else {
+                sum += part[q][k];
               }
-            v[k] = acc_value<kF8>(sum);
-            if constexpr (!kBlock)
-              v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row)), __ldg(w_scale + (int64_t)m.e * N + n + k));
-          }
-          put_four<KIND>(y, (int64_t)row * ldy + n, v);
+            }
+          v[k] = acc_value<kF8>(sum);
+          if constexpr (!kBlock)
+            v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row)), __ldg(w_scale + (int64_t)m.e * N + n + k));
         }
+        put_four<KIND>(y, (int64_t)row * ldy + n, v);
       }
     }
+    // no CTA leaves while a peer still reads its partial sums.  Nothing is
+    // published, and what was read has been added up and stored, so the
+    // barrier need not wait for the stores (1300 cycles of it)
     __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer still reads its partial sums
+    cluster_sync_relaxed();
   }
   tc_fence_before();
   __syncthreads();
@@ -1027,8 +1067,8 @@ struct SplitPlan {
 
 // The split with the least cost.  One that splits tiles pays about 4 + S / 2
 // blocks for its two cluster barriers and the partial sums (11008 x 4096 at
-// one row: 16.7 us unsplit, 15.3 with S = 3, 15.0 with S = 6; 4096 x 4096 at
-// 128 rows: 16.5 us unsplit, 13.7, 11.8 and 10.8 with S = 2, 3 and 4, 13.8 with
+// one row: 14.6 us unsplit, 14.3 with S = 3, 14.1 with S = 6; 4096 x 4096 at
+// 128 rows: 13.8 us unsplit, 12.2, 11.4 and 10.7 with S = 2, 3 and 4, 14.0 with
 // S = 8, of which fewer clusters fit).  Every CTA of a split cluster gets items
 // (nk >= S), so that a tile's contributors are consecutive.
 template <GScale SC, OutKind KIND>
@@ -1049,14 +1089,15 @@ SplitPlan plan_split(int dev, int64_t tiles, int64_t nk) {
 
 template <GScale SC, OutKind KIND>
 cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t st) {
-  CUtensorMap tmA, tmA32, tmB;
+  CUtensorMap tmA, tmA64, tmA32, tmB;
   if (!make_code_tmap(&tmA32, a.xq, a.T, a.K, 32) || !make_code_tmap(&tmB, a.wq, a.E * a.N, a.K, 128))
     return cudaErrorInvalidValue;
-  tmA = tmA32;
-  // (a tile of no more than 96 rows is loaded by 32)
-  if (a.T > 96 && !make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
+  // (no tile has more rows than T: of T <= 32 and T <= 64 the larger maps stay unused)
+  tmA = tmA64 = tmA32;
+  if (a.T > 32 && !make_code_tmap(&tmA64, a.xq, a.T, a.K, 64)) return cudaErrorInvalidValue;
+  if (a.T > 64 && !make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
   return launch_pdl(grouped_split_kernel<SC, KIND>, dim3(plan.C * plan.S), dim3(kThreads), SplitSmem::kTotal, st,
-                    (unsigned)plan.S, tmA, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
+                    (unsigned)plan.S, tmA, tmA64, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
                     a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, plan.S, device_error_word());
 }
 
@@ -1064,16 +1105,19 @@ cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t 
 // device: the host reckons with rows spread evenly over as many groups as can
 // have any, and half a tile of each group's last one empty.
 int64_t row_tiles(const GroupedArgs &a, int64_t rows) {
-  if (a.offsets == nullptr) return (a.T + rows - 1) / rows;
-  const int64_t groups = a.E < a.T ? a.E : a.T;
+  const int64_t groups = a.offsets == nullptr ? 1 : a.E < a.T ? a.E : a.T;
+  if (groups <= 1) return (a.T + rows - 1) / rows;
   const int64_t spread = (2 * a.T + groups * rows) / (2 * rows);
   return spread > groups ? spread : groups;
 }
 
 // Pairs on 256 x 256 tiles or single CTAs on 128 x 128 ones: whichever's
-// busiest unit has less to do.  A block of a pair's tile takes 1.2 times as
-// long as one of a single's (block scales: 1.4 times, their sums waiting on
-// both CTAs), for four times the products; measured at 512 to 24576 rows.
+// busiest unit has less to do.  A block of a pair's tile takes 1.35 times as
+// long as one of a single's (block scales: 1.5 times, their sums waiting on
+// both CTAs), for four times the products.  Singles and pairs, INT8: 12.6 and
+// 15.4 us at 512 x 4096 x 4096, 20.6 and 16.4 at 1024 rows; 46.7 and 56.2 at
+// 1100 x 4096 x 11008, whose 80 pairs' tiles do not fit at once; 4000 rows of
+// 64 experts 2048 -> 1408, 35.9 and 46.4; 2000 of 8 4096 -> 4096, 51.6 and 42.1.
 template <GScale SC, OutKind KIND>
 cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   const int64_t nk = (a.K + kBlk - 1) / kBlk;
@@ -1085,7 +1129,7 @@ cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   if (cap > 0) {
     const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
     const int64_t blocks = (tiles + cap - 1) / cap * nk;
-    if (split.S == 0 || blocks * (SC == GScale::Block ? 14 : 12) < split.cost * 10) return run_pair<SC, KIND>(a, cap, st);
+    if (split.S == 0 || blocks * (SC == GScale::Block ? 30 : 27) < split.cost * 20) return run_pair<SC, KIND>(a, cap, st);
   }
   if (split.S == 0) return cudaErrorLaunchOutOfResources;
   return run_split<SC, KIND>(a, split, st);
