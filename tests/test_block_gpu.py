@@ -134,6 +134,21 @@ def test_smooth_quant_weight_block_bit_exact(dt, E, N, K, alpha):
     np.testing.assert_array_equal(q.cpu().numpy(), q_ref)
 
 
+def test_smooth_quant_weight_block_more_block_rows_than_a_grid_has():
+    # 65538 block rows: beyond a grid's second dimension
+    N, K = 65537 * B + 16, 16
+    w = torch.randn(N, K, generator=torch.Generator(DEV).manual_seed(9), device=DEV, dtype=torch.float16)
+    wq, ws, _, _ = sq.sq_smooth_quant_weight_e4m3_block(w)
+    pad = torch.zeros(blocks(N) * B, K, device=DEV)
+    pad[:N] = w.float()
+    top = pad.view(-1, B * K).abs().amax(1)
+    d = top / torch.full_like(top, 448)      # (by a Python number torch multiplies with the reciprocal)
+    assert torch.equal(ws[:, 0], d)
+    want = (pad.view(-1, B * K) / d[:, None]).view(-1, K)[:N].to(torch.float8_e4m3fn)
+    assert torch.equal(wq, want.view(torch.uint8))
+    assert sq.sq_check_device_error() == sq.SQ_OK
+
+
 def test_smooth_quant_weight_block_strided_and_dense_shapes():
     wide = synth.weights(512, 272, 5, torch.bfloat16, "nk").to(DEV)
     w = wide[:, 64:64 + 272]
