@@ -620,9 +620,10 @@ cudaError_t run_pair(const GroupedArgs &a, int cap, cudaStream_t st) {
 constexpr int kMaxSplit = 8;  // CTAs per cluster
 
 // A split tile that this CTA helps to add up: cnt contributors from rank ra on
-// (0: there is none), its expert, first row, rows and first channel.
+// (0: there is none), its expert, first row and first channel, and this CTA's
+// share [u0, u1) of its units (four channels of a row, 32 units a row).
 struct SplitTile {
-  int cnt, ra, e, row, rows, n;
+  int cnt, ra, e, row, n, u0, u1;
 };
 
 struct SplitSmem {
@@ -736,8 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this cluster's tiles c, c + C, ...; this CTA's items [w0, w1) of theirs
   const int rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int c = blockIdx.x / S, C = gridDim.x / S;
-  const int64_t items = (int64_t)max(0, (g.tile[E] - c + C - 1) / C) * nk;
-  const int64_t w0 = items * rank / S, w1 = items * (rank + 1) / S;
+  // (items * S < 2^31, see plan_split: 64-bit divisions take 1000 cycles here)
+  const uint32_t items = (uint32_t)max(0, (g.tile[E] - c + C - 1) / C) * nk;
+  const uint32_t w0 = items * rank / S, w1 = items * (rank + 1) / S;
 
   if (warp == 0 || warp == 2) {
     if (lane == 0) {
@@ -747,10 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
       Place p;
-      for (int64_t w = w0; w < w1 && ok;) {
-        const int lt = (int)(w / nk);
-        int kb = (int)(w % nk);
-        const int kend = (int)min((int64_t)nk, w1 - (int64_t)lt * nk);
+      for (uint32_t w = w0; w < w1 && ok;) {
+        const uint32_t lt = w / nk;
+        int kb = w - lt * nk;
+        const int kend = min(nk, (int)(w1 - lt * nk));
         p.find(g, E, c + lt * C, 128);
         const int row_a = p.row0 + p.mb * 128, row_b = p.e * N + p.nb * 128;
         // as many of the tile's rows as its group has: one box of 32, 64 or 128
@@ -806,18 +808,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = lane;
       SplitTile m{};
       if (S > 1 && w1 > w0) {
-        const int lt = (int)(slot == 0 ? w0 / nk : (w1 - 1) / nk);
-        const int64_t i0 = (int64_t)lt * nk, i1 = i0 + nk;
+        const uint32_t lt = slot == 0 ? w0 / nk : (w1 - 1) / nk, i0 = lt * nk, i1 = i0 + nk;
         if (slot == 0 ? i0 < w0 : (i0 >= w0 && i1 > w1)) {
           // its contributors: the CTAs with its first to its last item
-          m.ra = (int)(((i0 + 1) * S - 1) / items);
-          m.cnt = (int)((i1 * S - 1) / items) - m.ra + 1;
+          m.ra = ((i0 + 1) * S - 1) / items;
+          m.cnt = (i1 * S - 1) / items - m.ra + 1;
           Place p;
           p.find(g, E, c + lt * C, 128);
           m.e = p.e;
           m.row = p.row0 + p.mb * 128;
-          m.rows = min(128, p.rows - p.mb * 128);
           m.n = p.nb * 128;
+          const int units = min(128, p.rows - p.mb * 128) * 32;
+          m.u0 = units * (rank - m.ra) / m.cnt;
+          m.u1 = units * (rank - m.ra + 1) / m.cnt;
         }
       }
       split[slot] = m;
@@ -835,6 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     out.lane = lane;
     uint32_t ab = 0, aphase = 0, stage = 0, phase = 0;
     bool ok = true, parked = false, parked_row = false;
+    // the last tile's sums go to slot 0 (begun by an earlier CTA) or to slot 1
+    // (ended by a later one); worked out here, while the first block is loaded
+    const bool begun = w0 % nk != 0 && w0 / nk == (w1 - 1) / nk, ended = w1 % nk == 0;
     float2 acc[32];  // fp32 sums; for INT8 the bits of int32 sums
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -848,9 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         aphase ^= 1;
       }
     };
-    for (int64_t w = w0; w < w1;) {
-      const int lt = (int)(w / nk), kb0 = (int)(w % nk);
-      const int kend = (int)min((int64_t)nk, w1 - (int64_t)lt * nk);
+    for (uint32_t w = w0; w < w1;) {
+      const uint32_t lt = w / nk;
+      const int kb0 = w - lt * nk, kend = min(nk, (int)(w1 - lt * nk));
       p.find(g, E, c + lt * C, 128);
       out.row0 = p.row0 + p.mb * 128 + quarter * 32;
       out.row_end = p.row0 + p.rows;
@@ -970,9 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // swizzled by row; only the group's rows
       const int r = quarter * 32 + lane;
       uint4 *mine4 = reinterpret_cast<uint4 *>(smem) + r * 32;
-      const bool one = w0 / nk == (w1 - 1) / nk;  // the CTA's items are of one tile
-      if (w1 > w0 && out.row0 + lane < out.row_end && (w1 % nk != 0 || (one && w0 % nk != 0))) {
-        uint4 *d = mine4 + (one && w0 % nk != 0 ? 0 : 128 * 32);
+      if (w1 > w0 && out.row0 + lane < out.row_end && (!ended || begun)) {
+        uint4 *d = mine4 + (begun ? 0 : 128 * 32);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           d[(half * 16 + j) ^ (r & 7)] = make_uint4(__float_as_uint(acc[2 * j].x), __float_as_uint(acc[2 * j].y),
@@ -1000,11 +1005,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int slot = 0; slot < 2; ++slot) {
       const SplitTile m = split[slot];
       if (m.cnt == 0) continue;
-      const int u1 = m.rows * 32 * (rank - m.ra + 1) / m.cnt;  // four channels of one row each
-      for (int u = m.rows * 32 * (rank - m.ra) / m.cnt + threadIdx.x; u < u1; u += kThreads) {
+      for (int u = m.u0 + threadIdx.x; u < m.u1; u += kThreads) {
         const int r = u >> 5, row = m.row + r, n = m.n + (u & 31) * 4;
         const uint32_t at = smem_u32(smem) + (uint32_t)(r * 32 + ((u & 31) ^ (r & 7))) * 16;
         if (n >= N) continue;
+        float dx = 0.0f;
+        float4 dw = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (!kBlock) {
+          dx = __ldg(x_scale + row);
+          dw = __ldg(reinterpret_cast<const float4 *>(w_scale + (int64_t)m.e * N + n));
+        }
         uint32_t part[kMaxSplit][4];
 #pragma unroll
         for (int q = 0; q < kMaxSplit; ++q)
@@ -1030,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           v[k] = acc_value<kF8>(sum);
           if constexpr (!kBlock)
-            v[k] = __fmul_rn(__fmul_rn(v[k], __ldg(x_scale + row)), __ldg(w_scale + (int64_t)m.e * N + n + k));
+            v[k] = __fmul_rn(__fmul_rn(v[k], dx), k == 0 ? dw.x : k == 1 ? dw.y : k == 2 ? dw.z : dw.w);
         }
         put_four<KIND>(y, (int64_t)row * ldy + n, v);
       }
@@ -1070,13 +1080,15 @@ struct SplitPlan {
 // one row: 14.6 us unsplit, 14.3 with S = 3, 14.1 with S = 6; 4096 x 4096 at
 // 128 rows: 13.8 us unsplit, 12.2, 11.4 and 10.7 with S = 2, 3 and 4, 14.0 with
 // S = 8, of which fewer clusters fit).  Every CTA of a split cluster gets items
-// (nk >= S), so that a tile's contributors are consecutive.
+// (nk >= S), so that a tile's contributors are consecutive.  `tiles` is what the
+// host reckons with, `most` what the offsets may lead to; a cluster's items are
+// counted in 32 bits (beyond that, 10^16 operations, pairs have it).
 template <GScale SC, OutKind KIND>
-SplitPlan plan_split(int dev, int64_t tiles, int64_t nk) {
+SplitPlan plan_split(int dev, int64_t tiles, int64_t most, int64_t nk) {
   SplitPlan best;
   for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
     const int64_t cap = split_capacity<SC, KIND>(dev, S), C = tiles < cap ? tiles : cap;
-    if (C <= 0) continue;
+    if (C <= 0 || (most / C + 1) * nk * S >= INT32_MAX) continue;
     const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 4 + S / 2 : 0);
     if (cost < best.cost) {
       best.S = S;
@@ -1124,7 +1136,8 @@ cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const SplitPlan split = plan_split<SC, KIND>(dev, row_tiles(a, 128) * ((a.N + 127) / 128), nk);
+  const int64_t ntn = (a.N + 127) / 128;
+  const SplitPlan split = plan_split<SC, KIND>(dev, row_tiles(a, 128) * ntn, (a.T / 128 + a.E) * ntn, nk);
   const int cap = pair_capacity<SC, KIND>(dev);
   if (cap > 0) {
     const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
