@@ -210,6 +210,20 @@ __device__ __forceinline__ void build_groups(const Groups &g, const int32_t *__r
   __syncthreads();
 }
 
+// Division by d, for dividends below 2^31: with 2^(l-1) < d <= 2^l and
+// m = floor(2^(31+l) / d) + 1, m d exceeds 2^(31+l) by at most d <= 2^l, so
+// w m / 2^(31+l) exceeds w / d by less than 1 / d and has the same floor.
+// (An integer division is some 100 cycles, and several in a row held back a
+// CTA's first load.)
+struct FastDiv {
+  uint32_t d, m, shift;
+  explicit FastDiv(uint32_t div) : d(div), shift(31) {
+    while ((1u << (shift - 31)) < d) ++shift;
+    m = (uint32_t)((1ull << shift) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t w) const { return (uint32_t)((uint64_t)w * m >> shift); }
+};
+
 // Where a tile lies; find() starts from the group of the tile before.
 struct Place {
   int e = 0, row0 = 0, rows = 0, mb = 0, nb = 0;
@@ -230,8 +244,8 @@ struct Place {
     row0 = g.row[e];
     rows = g.row[e + 1] - row0;
     const int nm = ceil_div_dev(rows, tile_rows), local = tile - g.tile[e];
-    nb = local / nm;
-    mb = local % nm;
+    nb = nm == 1 ? local : local / nm;
+    mb = local - nb * nm;
   }
 };
 
@@ -681,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
                          const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmB, const float *__restrict__ x_scale, const float *__restrict__ w_scale,
                          const int32_t *__restrict__ offsets, uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N,
-                         int K, int S, unsigned *err) {
+                         int K, FastDiv dS, FastDiv dC, FastDiv dnk, unsigned *err) {
   using L = SplitSmem;
   constexpr bool kF8 = SC != GScale::I8, kBlock = SC == GScale::Block;
   constexpr int kBufs = L::kBufs;
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   SplitTile *split = reinterpret_cast<SplitTile *>(g.tile + kMaxExperts + 1);  // [2]: slots 0 and 1
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int ntn = (N + 127) / 128, nk = (K + kBlk - 1) / kBlk;
+  const int ntn = (N + 127) / 128, nk = dnk.d, S = dS.d, C = dC.d;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -735,11 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   build_groups(g, offsets, E, T, 128, ntn);
 
   // this cluster's tiles c, c + C, ...; this CTA's items [w0, w1) of theirs
-  const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-  const int c = blockIdx.x / S, C = gridDim.x / S;
-  // (items * S < 2^31, see plan_split: 64-bit divisions take 1000 cycles here)
-  const uint32_t items = (uint32_t)max(0, (g.tile[E] - c + C - 1) / C) * nk;
-  const uint32_t w0 = items * rank / S, w1 = items * (rank + 1) / S;
+  // (items * S < 2^31, see plan_split)
+  const uint32_t c = dS.of(blockIdx.x), rank = blockIdx.x - c * S;
+  const uint32_t items = dC.of(max(0, g.tile[E] - (int)c + C - 1)) * nk;
+  const uint32_t w0 = dS.of(items * rank), w1 = dS.of(items * (rank + 1));
 
   if (warp == 0 || warp == 2) {
     if (lane == 0) {
@@ -750,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Place p;
       for (uint32_t w = w0; w < w1 && ok;) {
-        const uint32_t lt = w / nk;
+        const uint32_t lt = dnk.of(w);
         int kb = w - lt * nk;
         const int kend = min(nk, (int)(w1 - lt * nk));
         p.find(g, E, c + lt * C, 128);
@@ -795,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer ----------------
     mma_loop<1, kF8, kBlock, L::kStages, kBufs, L::kA, L::kB, 128>(
         smem_u32(sA), smem_u32(sB), full, empty, tfull, tempty, tmem_base, idesc8<kF8>(128, 128), w1 - w0, nk,
-        nk - (int)(w0 % nk), abort_flag, err);
+        nk - (int)(w0 - dnk.of(w0) * nk), abort_flag, err);
     // every MMA issued above must finish before TMEM is released
     if (elect_one()) {
       umma_commit(drain);
@@ -808,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = lane;
       SplitTile m{};
       if (S > 1 && w1 > w0) {
-        const uint32_t lt = slot == 0 ? w0 / nk : (w1 - 1) / nk, i0 = lt * nk, i1 = i0 + nk;
+        const uint32_t lt = dnk.of(slot == 0 ? w0 : w1 - 1), i0 = lt * nk, i1 = i0 + nk;
         if (slot == 0 ? i0 < w0 : (i0 >= w0 && i1 > w1)) {
           // its contributors: the CTAs with its first to its last item
           m.ra = ((i0 + 1) * S - 1) / items;
@@ -840,7 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, parked = false, parked_row = false;
     // the last tile's sums go to slot 0 (begun by an earlier CTA) or to slot 1
     // (ended by a later one); worked out here, while the first block is loaded
-    const bool begun = w0 % nk != 0 && w0 / nk == (w1 - 1) / nk, ended = w1 % nk == 0;
+    const uint32_t t0 = dnk.of(w0), t1 = w1 > w0 ? dnk.of(w1 - 1) : t0;
+    const bool begun = w0 != t0 * nk && t0 == t1, ended = w1 == (t1 + 1) * nk;
     float2 acc[32];  // fp32 sums; for INT8 the bits of int32 sums
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
@@ -855,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (uint32_t w = w0; w < w1;) {
-      const uint32_t lt = w / nk;
+      const uint32_t lt = dnk.of(w);
       const int kb0 = w - lt * nk, kend = min(nk, (int)(w1 - lt * nk));
       p.find(g, E, c + lt * C, 128);
       out.row0 = p.row0 + p.mb * 128 + quarter * 32;
@@ -1081,14 +1095,14 @@ struct SplitPlan {
 // 128 rows: 13.8 us unsplit, 12.2, 11.4 and 10.7 with S = 2, 3 and 4, 14.0 with
 // S = 8, of which fewer clusters fit).  Every CTA of a split cluster gets items
 // (nk >= S), so that a tile's contributors are consecutive.  `tiles` is what the
-// host reckons with, `most` what the offsets may lead to; a cluster's items are
-// counted in 32 bits (beyond that, 10^16 operations, pairs have it).
+// host reckons with, `most` what the offsets may lead to; tiles and a cluster's
+// items are counted in 31 bits (beyond that, 10^16 operations, pairs have it).
 template <GScale SC, OutKind KIND>
 SplitPlan plan_split(int dev, int64_t tiles, int64_t most, int64_t nk) {
   SplitPlan best;
   for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
     const int64_t cap = split_capacity<SC, KIND>(dev, S), C = tiles < cap ? tiles : cap;
-    if (C <= 0 || (most / C + 1) * nk * S >= INT32_MAX) continue;
+    if (C <= 0 || most > INT32_MAX / 2 || (most / C + 1) * nk * S >= INT32_MAX) continue;
     const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 4 + S / 2 : 0);
     if (cost < best.cost) {
       best.S = S;
@@ -1110,7 +1124,8 @@ cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t 
   if (a.T > 64 && !make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
   return launch_pdl(grouped_split_kernel<SC, KIND>, dim3(plan.C * plan.S), dim3(kThreads), SplitSmem::kTotal, st,
                     (unsigned)plan.S, tmA, tmA64, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
-                    a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, plan.S, device_error_word());
+                    a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, FastDiv(plan.S), FastDiv(plan.C), FastDiv((uint32_t)((a.K + kBlk - 1) / kBlk)),
+                    device_error_word());
 }
 
 // Row tiles of `rows` rows each over all groups.  The groups' sizes are on the
