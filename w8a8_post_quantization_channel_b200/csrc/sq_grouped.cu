@@ -1091,8 +1091,8 @@ struct SplitPlan {
 
 // The split with the least cost.  One that splits tiles pays about 4 + S / 2
 // blocks for its two cluster barriers and the partial sums (11008 x 4096 at
-// one row: 14.6 us unsplit, 14.3 with S = 3, 14.1 with S = 6; 4096 x 4096 at
-// 128 rows: 13.8 us unsplit, 12.2, 11.4 and 10.7 with S = 2, 3 and 4, 14.0 with
+// one row: 14.1 us unsplit, 13.1 with S = 3, 12.9 with S = 6; 4096 x 4096 at
+// one row: 12.1 us unsplit, 8.7, 7.8 and 7.1 with S = 2, 3 and 4, 8.7 with
 // S = 8, of which fewer clusters fit).  Every CTA of a split cluster gets items
 // (nk >= S), so that a tile's contributors are consecutive.  `tiles` is what the
 // host reckons with, `most` what the offsets may lead to; tiles and a cluster's
@@ -1141,10 +1141,10 @@ int64_t row_tiles(const GroupedArgs &a, int64_t rows) {
 // Pairs on 256 x 256 tiles or single CTAs on 128 x 128 ones: whichever's
 // busiest unit has less to do.  A block of a pair's tile takes 1.35 times as
 // long as one of a single's (block scales: 1.5 times, their sums waiting on
-// both CTAs), for four times the products.  Singles and pairs, INT8: 12.6 and
-// 15.4 us at 512 x 4096 x 4096, 20.6 and 16.4 at 1024 rows; 46.7 and 56.2 at
+// both CTAs), for four times the products.  Singles and pairs, INT8: 12.5 and
+// 15.1 us at 512 x 4096 x 4096, 20.1 and 16.2 at 1024 rows; 47.1 and 56.3 at
 // 1100 x 4096 x 11008, whose 80 pairs' tiles do not fit at once; 4000 rows of
-// 64 experts 2048 -> 1408, 35.9 and 46.4; 2000 of 8 4096 -> 4096, 51.6 and 42.1.
+// 64 experts 2048 -> 1408, 35.4 and 46.8; 2000 of 8 4096 -> 4096, 52.6 and 42.6.
 template <GScale SC, OutKind KIND>
 cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   const int64_t nk = (a.K + kBlk - 1) / kBlk;
