@@ -305,3 +305,18 @@ def test_a_mixture_layer_end_to_end(T):
     room = torch.zeros(T, K, dtype=torch.float64, device=DEV).index_add_(0, token, yb * g)
     assert torch.all((out.double() - want).abs() <= room + 1e-5 * want.abs())
     assert sq.sq_check_device_error() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("scale", ["i8", "e4m3", "block"])
+@pytest.mark.parametrize("sizes", [[1, 5, 17, 31, 3, 29, 8, 23], [33, 63, 40, 1, 127, 97, 65, 100]])
+def test_split_tiles_of_ragged_groups(scale, sizes):
+    # 256 tiles of 32 blocks over clusters whose CTAs hold the end of one tile
+    # and the beginning of another, of groups that end inside a warp's 32 rows
+    N, K = 4096, 4096
+    ops = codes(sum(sizes), len(sizes), N, K, scale, seed=31)
+    off = offsets_of(sizes)
+    y = CALL[scale](*ops, off, torch.float32)
+    check(y, *ops, off, scale, "f32")
+    for _ in range(5):
+        assert torch.equal(y, CALL[scale](*ops, off, torch.float32))
+    assert sq.sq_check_device_error() == sq.SQ_OK

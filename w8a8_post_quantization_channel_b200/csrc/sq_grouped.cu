@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   tc_fence_before();
+  __syncwarp();  // (thread 0 has just set up the barriers alone)
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  __syncwarp();  // (of the loaders one lane has worked)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer's shared memory and TMEM stay live until the leader is done
@@ -970,6 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (w < w1) {  // the end of a tile begun by an earlier CTA, with more to come: parked in TMEM
         parked = true;
         parked_row = out.row0 + lane < out.row_end;
+        __syncwarp();  // (lane 0 has just released the accumulator alone; TMEM accesses take the whole warp)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t r[16];
@@ -998,15 +1001,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __float_as_uint(acc[2 * j + 1].x), __float_as_uint(acc[2 * j + 1].y));
       }
       if (parked) {
+        // all of it before the stores, which some lanes make alone
+        uint32_t v[4][16];
+        __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[16];
-          tmem_ld16(taddr + kBufs * 128 + q * 16, v);
-          tmem_ld_wait();
-          if (parked_row)
+        for (int q = 0; q < 4; ++q) tmem_ld16(taddr + kBufs * 128 + q * 16, v[q]);
+        tmem_ld_wait();
+        if (parked_row) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mine4[(half * 16 + q * 4 + j) ^ (r & 7)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 16; ++j)
+            mine4[(half * 16 + j) ^ (r & 7)] =
+                make_uint4(v[j / 4][4 * (j % 4)], v[j / 4][4 * (j % 4) + 1], v[j / 4][4 * (j % 4) + 2], v[j / 4][4 * (j % 4) + 3]);
         }
       }
     }
