@@ -362,8 +362,12 @@ sq_status sq_w8a8_accumulate_e4m3(const uint8_t *xq, const uint8_t *wq, int64_t 
  *     p_tnb = sum_{j in block b} xq_tj wq_nj,
  *   p in fp32 on the tensor cores, the sum over blocks by fp32 fused
  *   multiply-adds in an order that depends on the shape alone: within
- *   (KB + 12) * 2^-23 * sum_j |x_j w_j| (x, w the dequantized values) of
- *   the exact sum, and the same bits on every call.
+ *   (KB + 12) * 2^-23 * sum_j |x_j w_j| + KB * 2^-125 (x, w the dequantized
+ *   values) of the exact sum, and the same bits on every call.  The second
+ *   term is what products of scales below fp32's normal range lose: each is
+ *   off by at most 2^-150, and |p| <= 128 * 448^2 < 2^25.  Both hold while
+ *   every product of scales and sum_j |x_j w_j| is below 2^127: a product
+ *   of scales that overflows gives Inf or NaN, even for a block of zeros.
  *   M == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N.  No workspace.
  */
 sq_status sq_quant_act_e4m3_block(const void *x, sq_dtype xt, int64_t M, int64_t K,

@@ -325,3 +325,24 @@ def test_codes_next_to_e4m3_midpoints(kind):
     q_ref, s_ref = oracle_weight(x[None])
     np.testing.assert_array_equal(s.cpu().numpy(), s_ref[0])
     np.testing.assert_array_equal(q.cpu().numpy(), q_ref[0])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (40, 272, 784), (333, 1040, 2064), (2048, 1536, 1024)])
+def test_linear_block_scale_products_at_the_ends_of_the_range(M, N, K):
+    # scale products below 2^-126 and up to 2^100 between ordinary ones.  A
+    # subnormal product is within 2^-150 of the exact one, times a block's sum
+    # of at most 128 * 448^2 < 2^25; adding below the normal range is off by
+    # 2^-150 per block: together under KB * 2^-125
+    xq, xs, wq, ws = operands(M, N, K, seed=23)
+    ws, xs = ws / ws.max(), xs / xs.max()
+    r = torch.arange(M, device=DEV) % 3
+    for dt in ("f32", "bf16"):
+        for w_shift, x_shift in ((-66, (-70, 0, 40)), (50, (50, -40, 0)), (-100, (-40, -49, -26))):
+            x_scale = xs * torch.exp2(torch.tensor(x_shift, device=DEV, dtype=torch.float32))[r][:, None]
+            w_scale = ws * 2.0 ** w_shift
+            y = sq.sq_w8a8_linear_e4m3_block(xq, x_scale, wq, w_scale, DT[dt])
+            x, w = dequantized(xq, x_scale, 1), dequantized(wq, w_scale, B)
+            bound = block_bound(K) * (x.abs() @ w.abs().t()) + blocks(K) * 2.0 ** -125
+            bound = bound + half_step((x @ w.t()).abs() + bound, dt)
+            assert torch.all((y.double() - x @ w.t()).abs() <= bound), (dt, w_shift)
+    assert sq.sq_check_device_error() == sq.SQ_OK
