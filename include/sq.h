@@ -361,7 +361,8 @@ sq_status sq_w8a8_accumulate_e4m3(const uint8_t *xq, const uint8_t *wq, int64_t 
  *     y_tn = round_yt(sum_b fl(x_scale_tb * w_scale_[n/128]b) * p_tnb),
  *     p_tnb = sum_{j in block b} xq_tj wq_nj,
  *   p in fp32 on the tensor cores, the sum over blocks by fp32 fused
- *   multiply-adds in an order that depends on the shape alone: within
+ *   multiply-adds in an order that depends on the shape and on the device's
+ *   SMs alone: within
  *   (KB + 12) * 2^-23 * sum_j |x_j w_j| + KB * 2^-125 (x, w the dequantized
  *   values) of the exact sum, and the same bits on every call.  The second
  *   term is what products of scales below fp32's normal range lose: each is
@@ -404,8 +405,9 @@ sq_status sq_w8a8_linear_e4m3_block(const uint8_t *xq, const float *x_scale,
  *   rows within the bound of sq_w8a8_linear_e4m3.
  * sq_w8a8_linear_grouped_e4m3_block: block scales, x_scale [T][KB], w_scale
  *   [E][NB][KB], each group's rows within sq_w8a8_linear_e4m3_block's bound.
- * The E4M3 sums' order depends on T, E, N, K and the offsets alone: the same
- * bits on every call.
+ * The E4M3 sums' order depends on T, E, N, K, the offsets and the device's SMs
+ * (how many clusters of CTAs they hold at once) alone: the same bits on every
+ * call on one kind of device.
  * T == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N, E * N < 2^31.
  * E <= 1024, T <= 2^31 - 1024 and fewer than 2^31 tiles of 128 x 128 in Y,
  * else SQ_ERR_UNSUPPORTED (the last two for sq_w8a8_linear_e4m3_block too).
