@@ -409,8 +409,9 @@ sq_status sq_w8a8_linear_e4m3_block(const uint8_t *xq, const float *x_scale,
  * (how many clusters of CTAs they hold at once) alone: the same bits on every
  * call on one kind of device.
  * T == 0 is a no-op.  K % 16 == 0, N % 16 == 0, ldy >= N, E * N < 2^31.
- * E <= 1024, T <= 2^31 - 1024 and fewer than 2^31 tiles of 128 x 128 in Y,
- * else SQ_ERR_UNSUPPORTED (the last two for sq_w8a8_linear_e4m3_block too).
+ * E <= 1024, each of T, E * N and K at most 2^31 - 1024, and fewer than 2^31
+ * tiles of 128 x 128 in Y, else SQ_ERR_UNSUPPORTED (all but the first for
+ * sq_w8a8_linear_e4m3_block too).
  * offsets is 4-byte aligned.  No workspace.
  */
 sq_status sq_w8a8_linear_grouped(const int8_t *xq, const float *x_scale,

@@ -87,3 +87,17 @@ def test_binding_refuses_what_it_cannot_pass_on():
     with pytest.raises(ValueError):
         sq.sq_w8a8_linear_grouped(u8.to(torch.int8), torch.zeros(4), u8, torch.zeros(1, 4),
                                   torch.zeros(2, dtype=torch.int32))
+
+
+def test_widths_whose_last_tile_passes_2_31():
+    # counted in 32 bits on the device, a tile's last column or channel would wrap
+    big = 1 << 31
+    call = _caller(sq.lib().sq_w8a8_linear_e4m3_block,
+                   dict(xq=A16, xs=A16, wq=A16, ws=A16, M=1, N=16, K=16, y=A16, yt=sq.SQ_BF16, ldy=big, st=None))
+    for wide in (dict(N=big - 16), dict(N=big - 1008), dict(K=big - 16), dict(K=big - 1008)):
+        assert call(**wide) == UNS, wide
+    for name in ("sq_w8a8_linear_grouped", "sq_w8a8_linear_grouped_e4m3", "sq_w8a8_linear_grouped_e4m3_block"):
+        call = _caller(getattr(sq.lib(), name), dict(xq=A16, xs=A16, wq=A16, ws=A16, off=A16, T=1, E=1, N=16, K=16,
+                                                     y=A16, yt=sq.SQ_F32, ldy=big, st=None))
+        for wide in (dict(N=big - 16), dict(K=big - 16), dict(E=23, N=(big // 23) // 16 * 16)):
+            assert call(**wide) == UNS, (name, wide)

@@ -411,8 +411,10 @@ static sq_status grouped_impl(const void *xq, const float *x_scale, const void *
   if (!valid_vec(wq) || !valid_vec(w_scale)) return SQ_ERR_INVALID_ARG;
   if (grouped && (offsets == nullptr || (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0)) return SQ_ERR_INVALID_ARG;
   if (E > sq::kMaxExperts) return SQ_ERR_UNSUPPORTED;
-  // tiles of 128 x 128 are numbered in 32 bits, and a tile's rows may pass T
-  if ((T / 128 + E) * ((N + 127) / 128) >= kMaxDim || T > kMaxDim - 1024) return SQ_ERR_UNSUPPORTED;
+  // tiles of 128 x 128 are numbered in 32 bits, and so are a tile's rows,
+  // columns and channels, which may pass T, E * N and K
+  if ((T / 128 + E) * ((N + 127) / 128) >= kMaxDim) return SQ_ERR_UNSUPPORTED;
+  if (T > kMaxDim - 1024 || E * N > kMaxDim - 1024 || K > kMaxDim - 1024) return SQ_ERR_UNSUPPORTED;
   if (T == 0) return SQ_OK;
   if (!valid_vec(xq) || !valid_vec(x_scale) || !valid_vec(y)) return SQ_ERR_INVALID_ARG;
   sq::GroupedArgs a{};
