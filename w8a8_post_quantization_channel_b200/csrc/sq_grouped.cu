@@ -14,6 +14,7 @@
 // The groups' sizes stay on the device: each CTA reads the offsets and forms
 // the prefix sums of the groups' tile counts, and tiles are numbered over
 // all groups.
+#include "sq_capacity.h"
 #include "sq_common.cuh"
 #include "sq_internal.h"
 
@@ -570,40 +571,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Clusters of `size` CTAs of a kernel (one CTA per SM) that can be resident at
-// once, after raising its shared-memory limit; 0 if none or a query fails.
-int resident_clusters(const void *kern, int size, uint32_t smem) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
+// Clusters of `size` CTAs of a kernel (one CTA per SM) that `dev`, the current
+// device, holds at once, after raising the kernel's shared-memory limit.
+cudaError_t resident_clusters(const void *kern, int dev, int size, uint32_t smem, int *n) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && size == 1) {
+    e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  } else if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(n, kern, &cfg);
   }
-  if (size == 1) return num_sms();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = size;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
+  if (e != cudaSuccess) cudaGetLastError();
+  if (e == cudaErrorInvalidClusterSize) {  // a size that this device never runs
+    *n = 0;
+    e = cudaSuccess;
   }
-  return n;
+  return e;
 }
 
 template <GScale SC, OutKind KIND>
-int pair_capacity(int dev) {
-  static int cache[64] = {};  // per device, capacity + 1
-  int &c = cache[dev & 63];
-  if (c == 0)
-    c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_pair_kernel<SC, KIND>), 2, PairTileSmem::kTotal);
-  return c - 1;
+cudaError_t pair_capacity(int dev, int *n) {
+  static CapacityCache cache;
+  const void *kern = reinterpret_cast<const void *>(grouped_pair_kernel<SC, KIND>);
+  return cache.get(dev, n, [&](int *c) { return resident_clusters(kern, dev, 2, PairTileSmem::kTotal, c); });
 }
 
 template <GScale SC, OutKind KIND>
@@ -1079,12 +1079,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <GScale SC, OutKind KIND>
-int split_capacity(int dev, int S) {
-  static int cache[64][kMaxSplit + 1] = {};  // per device and size, capacity + 1
-  int &c = cache[dev & 63][S];
-  if (c == 0)
-    c = 1 + resident_clusters(reinterpret_cast<const void *>(grouped_split_kernel<SC, KIND>), S, SplitSmem::kTotal);
-  return c - 1;
+cudaError_t split_capacity(int dev, int S, int *n) {
+  static CapacityCache cache[kMaxSplit + 1];
+  const void *kern = reinterpret_cast<const void *>(grouped_split_kernel<SC, KIND>);
+  return cache[S].get(dev, n, [&](int *c) { return resident_clusters(kern, dev, S, SplitSmem::kTotal, c); });
 }
 
 // How the split kernel is laid over the SMs: C clusters of S CTAs, and the
@@ -1103,10 +1101,13 @@ struct SplitPlan {
 // host reckons with, `most` what the offsets may lead to; tiles and a cluster's
 // items are counted in 31 bits (beyond that, 10^16 operations, pairs have it).
 template <GScale SC, OutKind KIND>
-SplitPlan plan_split(int dev, int64_t tiles, int64_t most, int64_t nk) {
+cudaError_t plan_split(int dev, int64_t tiles, int64_t most, int64_t nk, SplitPlan *plan) {
   SplitPlan best;
   for (int S = 1; S <= kMaxSplit && S <= nk; ++S) {
-    const int64_t cap = split_capacity<SC, KIND>(dev, S), C = tiles < cap ? tiles : cap;
+    int cap = 0;
+    const cudaError_t e = split_capacity<SC, KIND>(dev, S, &cap);
+    if (e != cudaSuccess) return e;
+    const int64_t C = tiles < cap ? tiles : cap;
     if (C <= 0 || most > INT32_MAX / 2 || (most / C + 1) * nk * S >= INT32_MAX) continue;
     const int64_t cost = ((tiles + C - 1) / C * nk + S - 1) / S + (S > 1 ? 4 + S / 2 : 0);
     if (cost < best.cost) {
@@ -1115,7 +1116,8 @@ SplitPlan plan_split(int dev, int64_t tiles, int64_t most, int64_t nk) {
       best.cost = cost;
     }
   }
-  return best;
+  *plan = best;
+  return cudaSuccess;
 }
 
 template <GScale SC, OutKind KIND>
@@ -1157,8 +1159,12 @@ cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int64_t ntn = (a.N + 127) / 128;
-  const SplitPlan split = plan_split<SC, KIND>(dev, row_tiles(a, 128) * ntn, (a.T / 128 + a.E) * ntn, nk);
-  const int cap = pair_capacity<SC, KIND>(dev);
+  SplitPlan split;
+  e = plan_split<SC, KIND>(dev, row_tiles(a, 128) * ntn, (a.T / 128 + a.E) * ntn, nk, &split);
+  if (e != cudaSuccess) return e;
+  int cap = 0;
+  e = pair_capacity<SC, KIND>(dev, &cap);
+  if (e != cudaSuccess) return e;
   if (cap > 0) {
     const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
     const int64_t blocks = (tiles + cap - 1) / cap * nk;
