@@ -1,7 +1,7 @@
 // sq_binding.cpp -- native marshalling for the block-scaled and the grouped
 // calls: checks tensors, allocates results on the current stream and calls
 // libsq's C functions.  In Python the same steps take longer than the launch
-// that they lead to (a single-token linear: 9.5 us of host time, 3.8 here).
+// that they lead to (a single-token linear: 9.5 us of host time, 4.2 here).
 //
 // Each function returns its result, or the call's status (an int) when it is
 // not SQ_OK; the Python side turns that into an SqError.  A tensor that does
@@ -83,6 +83,21 @@ at::Tensor given_or_new(PyObject *o, const char *name, at::ScalarType type, at::
   return fresh(type, shape, device);
 }
 
+// The library's call without the interpreter's lock, as under ctypes: a launch
+// waits where the stream's queue is full, and what empties the queue may need
+// another Python thread (a host callback).
+struct Unlocked {
+  PyThreadState *const state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked &) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F, class... A>
+sq_status unlocked(F f, A... a) {
+  const Unlocked scope;
+  return f(a...);
+}
+
 PyObject *status(sq_status s) { return PyLong_FromLong((long)s); }
 PyObject *wrap_or_none(const at::Tensor &t) {
   if (t.defined()) return THPVariable_Wrap(t);
@@ -127,10 +142,10 @@ PyObject *quant_act(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (inv != nullptr) expect(*inv, "inv_smooth", at::kFloat, {K}, dev);
   const at::Tensor q = given_or_new(a[2], "xq", at::kByte, {M, K}, dev);
   const at::Tensor s = given_or_new(a[3], "x_scale", at::kFloat, {M, blocks(K)}, dev);
-  const sq_status r = api.quant_act(x.data_ptr(), dt, M, K, M > 1 ? x.stride(0) : K,
-                                    inv != nullptr ? inv->const_data_ptr<float>() : nullptr,
-                                    static_cast<uint8_t *>(q.data_ptr()), static_cast<float *>(s.data_ptr()),
-                                    stream_of(dev));
+  const sq_status r = unlocked(api.quant_act, x.data_ptr(), dt, M, K, M > 1 ? x.stride(0) : K,
+                               inv != nullptr ? inv->const_data_ptr<float>() : nullptr,
+                               static_cast<uint8_t *>(q.data_ptr()), static_cast<float *>(s.data_ptr()),
+                               stream_of(dev));
   if (r != SQ_OK) return status(r);
   return Py_BuildValue("NN", THPVariable_Wrap(q), THPVariable_Wrap(s));
   END_HANDLE_TH_ERRORS
@@ -167,9 +182,9 @@ PyObject *quant_weight(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (amax != nullptr || a[5] != Py_None) s = given_or_new(a[5], "smooth", at::kFloat, {K}, dev);
   if (amax != nullptr || a[6] != Py_None) inv = given_or_new(a[6], "inv_smooth", at::kFloat, {K}, dev);
   auto f32 = [](const at::Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; };
-  const sq_status r = api.quant_weight(w.data_ptr(), dt, E, N, K, ld,
-                                       amax != nullptr ? amax->const_data_ptr<float>() : nullptr, (float)alpha,
-                                       static_cast<uint8_t *>(q.data_ptr()), f32(sc), f32(s), f32(inv), stream_of(dev));
+  const sq_status r = unlocked(api.quant_weight, w.data_ptr(), dt, E, N, K, ld,
+                               amax != nullptr ? amax->const_data_ptr<float>() : nullptr, (float)alpha,
+                               static_cast<uint8_t *>(q.data_ptr()), f32(sc), f32(s), f32(inv), stream_of(dev));
   if (r != SQ_OK) return status(r);
   return Py_BuildValue("NNNN", THPVariable_Wrap(q), THPVariable_Wrap(sc), wrap_or_none(s), wrap_or_none(inv));
   END_HANDLE_TH_ERRORS
@@ -237,14 +252,15 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const float *px = xs.const_data_ptr<float>(), *pw = ws.const_data_ptr<float>();
   void *const q = xq.data_ptr(), *const v = wq.data_ptr(), *const out = y.data_ptr();
   const sq_stream_t st = stream_of(dev);
+  auto *const q8 = static_cast<uint8_t *>(q), *const v8 = static_cast<uint8_t *>(v);
   sq_status r;
   if (kind == 0) {
-    r = api.linear_block(static_cast<uint8_t *>(q), px, static_cast<uint8_t *>(v), pw, T, N, K, out, yt, ldy, st);
+    r = unlocked(api.linear_block, q8, px, v8, pw, T, N, K, out, yt, ldy, st);
   } else if (kind == 1) {
-    r = api.grouped_i8(static_cast<int8_t *>(q), px, static_cast<int8_t *>(v), pw, off, T, E, N, K, out, yt, ldy, st);
+    r = unlocked(api.grouped_i8, static_cast<int8_t *>(q), px, static_cast<int8_t *>(v), pw, off, T, E, N, K, out, yt,
+                 ldy, st);
   } else {
-    const auto f = kind == 2 ? api.grouped_e4m3 : api.grouped_block;
-    r = f(static_cast<uint8_t *>(q), px, static_cast<uint8_t *>(v), pw, off, T, E, N, K, out, yt, ldy, st);
+    r = unlocked(kind == 2 ? api.grouped_e4m3 : api.grouped_block, q8, px, v8, pw, off, T, E, N, K, out, yt, ldy, st);
   }
   if (r != SQ_OK) return status(r);
   return THPVariable_Wrap(y);
