@@ -67,16 +67,14 @@ def library_path() -> str:
 
 
 def lib() -> ctypes.CDLL:
-    """Loads libsq.so (building it in-tree first when it is missing or stale)."""
+    """Loads libsq.so (building it in-tree first when it is missing or made from other sources)."""
     global _lib
     if _lib is None:
         from . import build as _build
         try:
             path = _build.build()
-        except Exception as e:  # no nvcc: only an existing library will do
-            if not os.path.exists(_LIB_PATH):
-                raise RuntimeError(f"libsq.so is missing and cannot be built: {e}") from e
-            path = _LIB_PATH
+        except Exception as e:  # no nvcc: only a library made from these sources will do
+            raise RuntimeError(f"libsq.so is missing or made from other sources, and cannot be built: {e}") from e
         L = ctypes.CDLL(path)
         vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         sigs = {
@@ -434,16 +432,16 @@ _native = None
 
 
 def _marshal():
-    """The native part of this binding (built in-tree when it is missing or stale)."""
+    """The native part of this binding (built in-tree when it is missing, made
+    from other sources, or for another torch or interpreter)."""
     global _native
     if _native is None:
         lib()
         from . import build as _build
         try:
             _build.build_binding()
-        except Exception as e:  # no compiler: only an existing one will do
-            if not os.path.exists(_build.BINDING):
-                raise RuntimeError(f"_binding.so is missing and cannot be built: {e}") from e
+        except Exception as e:  # no compiler: only one made from these sources, for this torch, will do
+            raise RuntimeError(f"_binding.so is missing or does not fit, and cannot be built: {e}") from e
         from . import _binding as native
         native.init(_LIB_PATH)
         _native = native

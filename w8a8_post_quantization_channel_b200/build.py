@@ -7,6 +7,8 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
+import mmap
 import os
 import shutil
 import subprocess
@@ -36,10 +38,30 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _deps_mtime() -> float:
+def _sources() -> list[str]:
+    """What libsq.so is made from."""
     files = glob.glob(os.path.join(CSRC, "*.cu*")) + glob.glob(os.path.join(CSRC, "*.h"))
-    files += glob.glob(os.path.join(INCLUDE, "*.h"))
-    return max(os.path.getmtime(f) for f in files)
+    return sorted(files + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _key(files: list[str], *more: str) -> str:
+    """A text of the files' contents and of `more`, which a binary carries: one
+    made from anything else is not taken for up to date, whatever its time."""
+    h = hashlib.sha256()
+    for part in (*(os.path.basename(f) for f in files), *more):
+        h.update(part.encode() + b"\0")
+    for f in files:
+        with open(f, "rb") as src:
+            h.update(hashlib.sha256(src.read()).digest())
+    return "sq-built-from:" + h.hexdigest()
+
+
+def _carries(path: str, key: str) -> bool:
+    try:
+        with open(path, "rb") as f, mmap.mmap(f.fileno(), 0, access=mmap.ACCESS_READ) as m:
+            return m.find(key.encode()) >= 0
+    except (OSError, ValueError):  # missing, or empty
+        return False
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -53,10 +75,20 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _binding_key() -> str:
+    import sysconfig
+
+    import torch
+    return _key([BINDING_SRC, os.path.join(INCLUDE, "sq.h")], torch.__version__, str(torch.version.git_version),
+                str(torch.compiled_with_cxx11_abi()), str(sysconfig.get_config_var("SOABI")))
+
+
 def build_binding(force: bool = False) -> str:
     """Compile _binding.so against the torch that runs this."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "sq.h")]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+    if not force and not os.path.exists(BINDING_SRC) and os.path.exists(BINDING):
+        return BINDING  # a tree without sources
+    key = _binding_key()
+    if not force and _carries(BINDING, key):
         return BINDING
     import sysconfig
 
@@ -64,7 +96,8 @@ def build_binding(force: bool = False) -> str:
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DSQ_BUILD_KEY="{key}"',
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
@@ -77,11 +110,15 @@ def build_binding(force: bool = False) -> str:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile every csrc/*.cu and link libsq.so (static cudart)."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and not _sources() and os.path.exists(LIB):
+        return LIB  # a tree without sources
+    flags = " ".join([*ARCH, *(f for f in NVFLAGS if f not in (INCLUDE, CSRC))])
+    key = _key(_sources(), flags)
+    if not force and _carries(LIB, key):
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
+    extra = [f'-DSQ_BUILD_KEY="{key}"'] + (["-Xptxas", "-v"] if verbose_ptxas else [])
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     tmp = LIB + f".tmp{os.getpid()}"

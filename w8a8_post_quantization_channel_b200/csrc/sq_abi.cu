@@ -54,6 +54,11 @@ unsigned *device_error_word() {
 
 namespace {
 
+// What this was built from, for build.py to find in the binary.
+#ifdef SQ_BUILD_KEY
+[[gnu::used]] const char kBuiltFrom[] = SQ_BUILD_KEY;
+#endif
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(int t) { return t == SQ_F32 || t == SQ_F16 || t == SQ_BF16; }
 int64_t dsize(sq_dtype t) { return t == SQ_F32 ? 4 : 2; }

@@ -23,6 +23,11 @@
 
 namespace {
 
+// What this was built from, for build.py to find in the binary.
+#ifdef SQ_BUILD_KEY
+[[gnu::used]] const char kBuiltFrom[] = SQ_BUILD_KEY;
+#endif
+
 struct Api {
   decltype(&sq_quant_act_e4m3_block) quant_act;
   decltype(&sq_smooth_quant_weight_e4m3_block) quant_weight;
