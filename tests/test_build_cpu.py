@@ -3,6 +3,8 @@ are there, against the torch and the interpreter that run; with stand-ins for
 the compilers."""
 import os
 import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -12,14 +14,22 @@ from w8a8_post_quantization_channel_b200 import build
 
 
 class Compilers:
-    """Stands in for subprocess.run: fails, and counts calls."""
+    """Stands in for subprocess.run: fails, or copies the true binary; counts calls."""
 
-    def __init__(self):
-        self.calls = 0
+    def __init__(self, result=None):
+        self.result, self.calls, self.inside, self.most = result, 0, 0, 0
 
     def __call__(self, cmd, **kw):
         self.calls += 1
-        return subprocess.CompletedProcess(cmd, 1, "", "no compiler here")
+        self.inside += 1
+        self.most = max(self.most, self.inside)
+        time.sleep(0.05)
+        self.inside -= 1
+        if self.result is None:
+            return subprocess.CompletedProcess(cmd, 1, "", "no compiler here")
+        with open(cmd[cmd.index("-o") + 1], "wb") as f:
+            f.write(self.result)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
 
 
 @pytest.fixture
@@ -81,6 +91,21 @@ def test_no_fallback_to_a_binding_that_does_not_fit(binding, monkeypatch):
     with pytest.raises(RuntimeError):
         sq._marshal()
     assert sq._native is None
+
+
+def test_builds_take_turns(binding):
+    path, _, binary = binding
+    run = Compilers(binary)
+    build.subprocess.run = run  # (put back with the fixture's)
+    threads = [threading.Thread(target=build.build_binding, args=(True,)) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert run.calls == 4 and run.most == 1
+    assert sorted(p.name for p in path.iterdir()) == ["_binding.so", "sq_binding.cpp"]
+    with open(path / "_binding.so", "rb") as f:
+        assert f.read() == binary
 
 
 def test_the_library_is_held_to_its_sources_too(tmp_path, monkeypatch):

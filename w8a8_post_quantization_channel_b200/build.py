@@ -6,6 +6,8 @@ Usage: python -m w8a8_post_quantization_channel_b200.build [--force]
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import glob
 import hashlib
 import mmap
@@ -64,6 +66,15 @@ def _carries(path: str, key: str) -> bool:
         return False
 
 
+@contextlib.contextmanager
+def _alone():
+    """One build of this tree at a time, over threads and processes."""
+    os.makedirs(OBJ, exist_ok=True)
+    with open(os.path.join(OBJ, "lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
+
+
 def _compile(src: str, extra: list[str]) -> str:
     obj = os.path.join(OBJ, os.path.basename(src) + ".o")
     cmd = [nvcc(), *ARCH, *NVFLAGS, *extra, "-c", src, "-o", obj]
@@ -87,25 +98,28 @@ def build_binding(force: bool = False) -> str:
     """Compile _binding.so against the torch that runs this."""
     if not force and not os.path.exists(BINDING_SRC) and os.path.exists(BINDING):
         return BINDING  # a tree without sources
-    key = _binding_key()
-    if not force and _carries(BINDING, key):
+    if not force and _carries(BINDING, _binding_key()):
         return BINDING
-    import sysconfig
+    with _alone():
+        key = _binding_key()
+        if not force and _carries(BINDING, key):  # made by another one meanwhile
+            return BINDING
+        import sysconfig
 
-    import torch
-    root = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(nvcc()))
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DSQ_BUILD_KEY="{key}"',
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
-           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc()))
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DSQ_BUILD_KEY="{key}"',
+               "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+               "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+               "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+        return BINDING
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -113,21 +127,23 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not _sources() and os.path.exists(LIB):
         return LIB  # a tree without sources
     flags = " ".join([*ARCH, *(f for f in NVFLAGS if f not in (INCLUDE, CSRC))])
-    key = _key(_sources(), flags)
-    if not force and _carries(LIB, key):
+    if not force and _carries(LIB, _key(_sources(), flags)):
         return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    extra = [f'-DSQ_BUILD_KEY="{key}"'] + (["-Xptxas", "-v"] if verbose_ptxas else [])
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+    with _alone():
+        key = _key(_sources(), flags)
+        if not force and _carries(LIB, key):  # made by another one meanwhile
+            return LIB
+        srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+        extra = [f'-DSQ_BUILD_KEY="{key}"'] + (["-Xptxas", "-v"] if verbose_ptxas else [])
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+            objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+        return LIB
 
 
 if __name__ == "__main__":
