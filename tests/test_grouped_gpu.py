@@ -320,3 +320,44 @@ def test_split_tiles_of_ragged_groups(scale, sizes):
     for _ in range(5):
         assert torch.equal(y, CALL[scale](*ops, off, torch.float32))
     assert sq.sq_check_device_error() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("scale", ["i8", "e4m3"])
+@pytest.mark.parametrize("T", [6, 300])
+def test_experts_quantized_by_the_dense_calls(scale, T):
+    """The documented way to the codes of INT8 and E4M3 experts: one dense
+    quantizer call over the stacked weights, its results viewed per expert.
+    Against the layer in 64 bits: an INT8 code is off by at most half a scale,
+    an E4M3 code by 2^-4 of its value or, below 2^-6, by 2^-10; the fp32
+    roundings of s, 1/s, x~, w~, their quotients and the dequantization are
+    under 20 of 2^-23 together, and the E4M3 sum is off by K/32 + 17 of them."""
+    E, K, N = 8, 528, 272
+    x = synth.activations(T, K, synth.outliers(K, frac=0.01, mult=60.0, seed=1), 2, torch.bfloat16).to(DEV)
+    w = synth.weights(K, E * N, 3, torch.bfloat16).reshape(E, N, K).to(DEV)
+    expert = torch.randint(0, E, (T,), generator=synth.gen(4)).to(DEV).sort().values
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device=DEV),
+                     torch.bincount(expert, minlength=E).cumsum(0)]).to(torch.int32)
+    amax = torch.zeros(K, device=DEV)
+    sq.sq_calib_absmax(x, amax)
+    i8 = scale == "i8"
+    quant_w, quant_x = ((sq.sq_smooth_quant_weight, sq.sq_quant_act) if i8 else
+                        (sq.sq_smooth_quant_weight_e4m3, sq.sq_quant_act_e4m3))
+    wq, ws, s, inv = quant_w(w.view(E * N, K), sq.SQ_W_NK, amax, 0.5)
+    xq, xs = quant_x(x, inv)
+    wq, ws = wq.view(E, N, K), ws.view(E, N)
+    y = CALL[scale](xq, xs, wq, ws, off, torch.float32)
+    check(y, xq, xs, wq, ws, off, scale, "f32")
+
+    def size_and_error(v, d):
+        v = v.abs()
+        return (v, (d / 2).expand_as(v)) if i8 else (v, v * 2.0 ** -4 + d * 2.0 ** -10)
+    ulps = ((0 if i8 else K / 32 + 17) + 20) * 2.0 ** -23
+    o = off.tolist()
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        exact = x[r].double() @ w[e].double().t()
+        xv, xe = size_and_error(x[r].double() * inv.double(), xs[r, None].double())
+        wv, we = size_and_error(w[e].double() * s.double(), ws[e, :, None].double())
+        room = xv @ we.t() + xe @ wv.t() + xe @ we.t() + ulps * ((xv + xe) @ (wv + we).t())
+        assert torch.all((y[r].double() - exact).abs() <= room), e
+    assert sq.sq_check_device_error() == sq.SQ_OK
