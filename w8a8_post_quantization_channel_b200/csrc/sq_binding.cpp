@@ -54,7 +54,8 @@ const at::Tensor &need(PyObject *o, const char *name) {
 }
 
 // t is a contiguous tensor of this type and shape on `device`.
-void expect(const at::Tensor &t, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Device &device) {
+void expect(const at::Tensor &t, const char *name, at::ScalarType type, at::IntArrayRef shape,
+            const at::Device &device) {
   TORCH_CHECK_VALUE(t.scalar_type() == type, name, ": dtype ", t.scalar_type(), " not supported (", type, ")");
   TORCH_CHECK_VALUE(t.sizes() == shape, name, " must have shape ", shape, ", not ", t.sizes());
   TORCH_CHECK_VALUE(t.device() == device, name, " must be on ", device, ", not ", t.device());
@@ -209,7 +210,8 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const at::Tensor &xq = need(a[1], "xq"), &xs = need(a[2], "x_scale"), &wq = need(a[3], "wq"),
                    &ws = need(a[4], "w_scale");
   rowmajor(xq, "xq");
-  TORCH_CHECK_VALUE(wq.dim() == (grouped ? 3 : 2), "wq must be a ", grouped ? "3-D tensor [E, N, K]" : "2-D tensor [N, K]");
+  TORCH_CHECK_VALUE(wq.dim() == (grouped ? 3 : 2), "wq must be a ",
+                    grouped ? "3-D tensor [E, N, K]" : "2-D tensor [N, K]");
   const at::Device dev = xq.device();
   const c10::cuda::CUDAGuard guard(dev);
   const int64_t T = xq.size(0), K = xq.size(1), E = grouped ? wq.size(0) : 1, N = wq.size(-2), KB = blocks(K);

@@ -23,7 +23,9 @@ namespace sq {
 namespace {
 
 constexpr int kBlk = 128;          // channels per scale block = K bytes per stage
-constexpr int kThreads = 384;      // TMA, MMA and two idle warps, then eight epilogue warps
+// Warps 0 and 2 load Xq and Wq, warp 1 issues the MMAs, warp 3 works out the
+// split tiles (idle with pairs), then eight epilogue warps.
+constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kStageBytes = 4096;  // an epilogue warp's output staging: 32 rows x 128 bytes
 
@@ -259,7 +261,6 @@ struct Place {
 template <OutKind KIND>
 struct RowStore {
   static constexpr int kEsz = KIND == OutKind::F32 ? 4 : 2;
-  static constexpr int kCols = 128 / kEsz;  // columns per staged row
   uint8_t *stage;
   uint8_t *y;
   int64_t ldy;
@@ -332,8 +333,9 @@ __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.
 
 // Persistent over 256 x 256 tiles of Y: a pair of CTAs works on one tile
 // (tcgen05 cta_group::2), each with 128 rows of Xq and half of the tile's rows
-// of Wq in its shared memory; the leader's MMA thread drives both.  Warps 0 and 2 load, warp 1 issues the MMAs, warps 4-11 (two per
-// TMEM lane quarter, each half of the columns) dequantize and store.
+// of Wq in its shared memory; the leader's MMA warp drives both.  Warps 0 and 2
+// load, warp 1 issues the MMAs, warps 4-11 (two per TMEM lane quarter, each
+// half of the columns) dequantize and store.
 template <GScale SC, OutKind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -407,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place p;
       for (int tile = unit; tile < tiles && ok; tile += units) {
         p.find(g, E, tile, kPairRows);
-        const int row = x ? p.row0 + p.mb * kPairRows + rank * 128 : p.e * N + p.nb * kPairCols + rank * (kPairCols / 2);
+        const int row = x ? p.row0 + p.mb * kPairRows + rank * 128
+                          : p.e * N + p.nb * kPairCols + rank * (kPairCols / 2);
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, err)) {
             ok = false;
@@ -509,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                acc[c * 8 + j] = ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])),
-                                          s2, acc[c * 8 + j]);
+                acc[c * 8 + j] = ffma2_rn(
+                    make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])), s2,
+                    acc[c * 8 + j]);
               if (c + 1 < kCols / 16) tmem_ld_wait();
             }
           }
@@ -695,7 +699,8 @@ __device__ __forceinline__ void put_four(uint8_t *y, int64_t i, const float (&v)
 template <GScale SC, OutKind KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
-                         const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmB, const float *__restrict__ x_scale, const float *__restrict__ w_scale,
+                         const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmB,
+                         const float *__restrict__ x_scale, const float *__restrict__ w_scale,
                          const int32_t *__restrict__ offsets, uint8_t *__restrict__ y, int64_t ldy, int T, int E, int N,
                          int K, FastDiv dS, FastDiv dC, FastDiv dnk, unsigned *err) {
   using L = SplitSmem;
@@ -937,8 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(taddr + ab * 128 + 32, r[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              acc[j] = make_float2(__uint_as_float(r[j / 16][2 * (j % 16)]), __uint_as_float(r[j / 16][2 * (j % 16) + 1]));
+            for (int j = 0; j < 32; ++j) {
+              const int h = j / 16, i = 2 * (j % 16);
+              acc[j] = make_float2(__uint_as_float(r[h][i]), __uint_as_float(r[h][i + 1]));
+            }
           }
           release();
         }
@@ -997,8 +1004,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 *d = mine4 + (begun ? 0 : 128 * 32);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          d[(half * 16 + j) ^ (r & 7)] = make_uint4(__float_as_uint(acc[2 * j].x), __float_as_uint(acc[2 * j].y),
-                                                    __float_as_uint(acc[2 * j + 1].x), __float_as_uint(acc[2 * j + 1].y));
+          d[(half * 16 + j) ^ (r & 7)] =
+              make_uint4(__float_as_uint(acc[2 * j].x), __float_as_uint(acc[2 * j].y),
+                         __float_as_uint(acc[2 * j + 1].x), __float_as_uint(acc[2 * j + 1].y));
       }
       if (parked) {
         // all of it before the stores, which some lanes make alone
@@ -1009,9 +1017,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         if (parked_row) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            mine4[(half * 16 + j) ^ (r & 7)] =
-                make_uint4(v[j / 4][4 * (j % 4)], v[j / 4][4 * (j % 4) + 1], v[j / 4][4 * (j % 4) + 2], v[j / 4][4 * (j % 4) + 3]);
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t *four = v[j / 4] + 4 * (j % 4);
+            mine4[(half * 16 + j) ^ (r & 7)] = make_uint4(four[0], four[1], four[2], four[3]);
+          }
         }
       }
     }
@@ -1130,9 +1139,9 @@ cudaError_t run_split(const GroupedArgs &a, const SplitPlan &plan, cudaStream_t 
   if (a.T > 32 && !make_code_tmap(&tmA64, a.xq, a.T, a.K, 64)) return cudaErrorInvalidValue;
   if (a.T > 64 && !make_code_tmap(&tmA, a.xq, a.T, a.K, 128)) return cudaErrorInvalidValue;
   return launch_pdl(grouped_split_kernel<SC, KIND>, dim3(plan.C * plan.S), dim3(kThreads), SplitSmem::kTotal, st,
-                    (unsigned)plan.S, tmA, tmA64, tmA32, tmB, a.x_scale, a.w_scale, a.offsets, static_cast<uint8_t *>(a.y),
-                    a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, FastDiv(plan.S), FastDiv(plan.C), FastDiv((uint32_t)((a.K + kBlk - 1) / kBlk)),
-                    device_error_word());
+                    (unsigned)plan.S, tmA, tmA64, tmA32, tmB, a.x_scale, a.w_scale, a.offsets,
+                    static_cast<uint8_t *>(a.y), a.ldy, (int)a.T, (int)a.E, (int)a.N, (int)a.K, FastDiv(plan.S),
+                    FastDiv(plan.C), FastDiv((uint32_t)((a.K + kBlk - 1) / kBlk)), device_error_word());
 }
 
 // Row tiles of `rows` rows each over all groups.  The groups' sizes are on the
@@ -1168,7 +1177,8 @@ cudaError_t run_grouped(const GroupedArgs &a, cudaStream_t st) {
   if (cap > 0) {
     const int64_t tiles = row_tiles(a, kPairRows) * ((a.N + kPairCols - 1) / kPairCols);
     const int64_t blocks = (tiles + cap - 1) / cap * nk;
-    if (split.S == 0 || blocks * (SC == GScale::Block ? 30 : 27) < split.cost * 20) return run_pair<SC, KIND>(a, cap, st);
+    if (split.S == 0 || blocks * (SC == GScale::Block ? 30 : 27) < split.cost * 20)
+      return run_pair<SC, KIND>(a, cap, st);
   }
   if (split.S == 0) return cudaErrorLaunchOutOfResources;
   return run_split<SC, KIND>(a, split, st);
